@@ -7,6 +7,7 @@ There is no fallback: if the library is missing or was built for another GPU the
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -29,7 +30,9 @@ __all__ = [
     "spark_bsa_gather_kv_meanpool", "spark_bsa_route_threshold", "spark_bsa_attend_var",
     "spark_bsa_set_wait_limit_ns", "spark_bsa_get_wait_limit_ns",
     "spark_bsa_host_staging_size_ex", "spark_bsa_fused_supported", "spark_bsa_forward_fused",
-    "spark_bsa_attend_fused",
+    "spark_bsa_attend_fused", "spark_qk_norm_rope", "spark_rope_frequencies",
+    "spark_attend_dense", "spark_attend_dense_workspace_size", "spark_attend_ranges",
+    "spark_bsa_workspace_size_joint", "spark_bsa_forward_joint",
 ]
 
 SPARK_BF16, SPARK_F32 = 0, 1
@@ -47,8 +50,11 @@ EXPORTED = [
     "spark_bsa_gather_kv_meanpool", "spark_bsa_route_threshold", "spark_bsa_attend_var",
     "spark_bsa_set_wait_limit_ns", "spark_bsa_get_wait_limit_ns",
     "spark_bsa_host_staging_size_ex", "spark_bsa_forward_host_ex", "spark_bsa_fused_supported",
-    "spark_bsa_forward_fused", "spark_bsa_attend_fused",
+    "spark_bsa_forward_fused", "spark_bsa_attend_fused", "spark_qk_norm_rope",
+    "spark_rope_frequencies", "spark_attend_dense", "spark_attend_dense_workspace_size",
+    "spark_attend_ranges", "spark_bsa_workspace_size_joint", "spark_bsa_forward_joint",
 ]
+ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
 REBLOCK_MODES = {"q_reuse_k": 0, "separate": 1}
 
 
@@ -137,6 +143,16 @@ def lib():
                                               _P, _P, _P, _P, _P]),
         "spark_bsa_attend_fp8": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _P, _P, _P, _I,
                                       _P, _P, _I, _P, _I, _I, _I, _I, _P, _I, _P, _P]),
+        "spark_qk_norm_rope": (_I, [_P, _P, _P, _I, _I, _I, _I, _P, _P, _P, _D, _P, _I, _I, _P,
+                                    _I, _P, _I, _D, _P, _P, _P, _P]),
+        "spark_rope_frequencies": (_I, [_P, _I, _D, _I, _D, _D, _P, _P]),
+        "spark_attend_dense_workspace_size": (_SZ, [_I, _I, _I, _I, _I]),
+        "spark_attend_dense": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _P, _I, _P, _P,
+                                    _SZ, _P, _P]),
+        "spark_attend_ranges": (_I, [_I, _I, _P, _P, _P, _P, _I, _P, _P, _P]),
+        "spark_bsa_workspace_size_joint": (_SZ, [_I, _I, _I, _I, _I, _D, _I]),
+        "spark_bsa_forward_joint": (_I, [_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _P, _P,
+                                         _I, _P, _I, _D, _P, _P, _P, _SZ, _P]),
         "spark_bsa_workspace_size_fp8": (_SZ, [_I, _I, _I, _I, _I, _D, _I]),
         "spark_bsa_forward_fp8": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _P, _P, _I,
                                        _P, _I, _D, _P, _P, _SZ, _P]),
@@ -857,3 +873,231 @@ def spark_bsa_forward_host(Q, K, V, q_perm, k_perm, q_offsets, k_offsets, topk_r
                                          workspace.numel(), sc, sh, sd)
     _check("spark_bsa_forward_host", st)
     return out
+
+
+# ------------------------------------------------ norm and rotation, dense attention
+
+def _on(dev):
+    """Makes `dev` current for a launch on one of its streams (a no-op when it is)."""
+    if dev.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return torch.cuda.device(dev)
+
+
+def _stream_of(dev, stream):
+    s = torch.cuda.current_stream(dev) if stream is None else stream
+    return ctypes.c_void_p(s.cuda_stream)
+
+
+def spark_rope_frequencies(axis_pairs, base=10000.0, scaling="none", factor=1.0, original=0.0):
+    """Rotation frequencies of the axes (fp32 CPU tensor of sum(axis_pairs)) and the factor for
+    rope_scale; scaling is "none", "linear", "ntk" or "yarn"."""
+    n = len(axis_pairs)
+    counts = (ctypes.c_int32 * max(n, 1))(*(int(p) for p in axis_pairs))
+    out = torch.empty(max(sum(max(int(p), 0) for p in axis_pairs), 1), dtype=torch.float32)
+    scale = ctypes.c_double(1.0)
+    st = lib().spark_rope_frequencies(counts, n, float(base), ROPE_SCALINGS[scaling],
+                                      float(factor), float(original), _ptr(out),
+                                      ctypes.byref(scale))
+    _check("spark_rope_frequencies", st)
+    return out[:sum(int(p) for p in axis_pairs)], scale.value
+
+
+def _need_rows(t, name, dtype, shape, device):
+    """Like _need for a tensor whose last dimension alone has to be contiguous."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype not in (dtype if isinstance(dtype, tuple) else (dtype,)):
+        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.dim() != 3 or (shape is not None and t.shape != shape):
+        raise ValueError(f"{name} must have the shape [H, N, d] of Q")
+    if t.stride(2) != 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+
+
+def spark_qk_norm_rope(Q, K=None, V=None, q_weight=None, k_weight=None, eps=1e-6, positions=None,
+                       inv_freq=None, axis_pairs=None, interleaved=False, rope_scale=1.0,
+                       Q_out=None, K_out=None, V_out=None, stream=None):
+    """Per-head RMS norm and position rotation of Q and K [H, N, d] (any head and token strides,
+    such as the transposed views of a fused projection's output), laid out contiguous; V is laid
+    out along.  Weights fp32 [d] (None: no norm); positions [N, axes] int32 or fp32; inv_freq
+    fp32 [pairs], axis_pairs the pairs of each axis (None: one axis).  Returns (Q_out, K_out,
+    V_out), None for what is absent."""
+    _need_rows(Q, "Q", (torch.bfloat16, torch.float32), None, None)
+    dev, dt = Q.device, Q.dtype
+    H, N, d = Q.shape
+    ins, outs, strides = (Q, K, V), [Q_out, K_out, V_out], []
+    for i, name in enumerate("QKV"):
+        if ins[i] is None:
+            if outs[i] is not None:
+                raise ValueError(f"{name}_out given without {name}")
+            strides += [0, 0]
+            continue
+        if i:
+            _need_rows(ins[i], name, dt, Q.shape, dev)
+        strides += [ins[i].stride(0), ins[i].stride(1)]
+        if outs[i] is None:
+            outs[i] = torch.empty(H, N, d, dtype=dt, device=dev)
+        else:
+            _need(outs[i], name + "_out", dt, dev)
+            if outs[i].shape != Q.shape:
+                raise ValueError(f"{name}_out must have the shape [H, N, d] of Q")
+    for name, w, x in (("q_weight", q_weight, Q), ("k_weight", k_weight, K)):
+        if w is not None:
+            _need(w, name, torch.float32, dev)
+            if w.shape != (d,) or x is None:
+                raise ValueError(f"{name} must have the shape [d] and its tensor be given")
+    pairs, naxes, counts, f32 = 0, 0, None, 0
+    if inv_freq is not None:
+        _need(inv_freq, "inv_freq", torch.float32, dev)
+        if positions is None:
+            raise ValueError("inv_freq needs positions")
+        _need(positions, "positions", (torch.int32, torch.float32), dev)
+        pairs = inv_freq.numel()
+        naxes = positions.shape[1] if positions.dim() == 2 else 1
+        if positions.dim() not in (1, 2) or positions.shape[0] != N:
+            raise ValueError("positions must have the shape [N, axes]")
+        axis_pairs = [pairs] if axis_pairs is None else axis_pairs
+        if len(axis_pairs) != naxes or sum(axis_pairs) != pairs:
+            raise ValueError("axis_pairs must give every axis of positions its pairs of inv_freq")
+        counts = (ctypes.c_int32 * naxes)(*axis_pairs)
+        f32 = int(positions.dtype == torch.float32)
+    elif positions is not None or axis_pairs is not None:
+        raise ValueError("positions and axis_pairs need inv_freq")
+    with _on(dev):
+        st = lib().spark_qk_norm_rope(
+            _ptr(Q), _ptr(K), _ptr(V), _code(dt), H, N, d, (ctypes.c_int64 * 6)(*strides),
+            _ptr(q_weight), _ptr(k_weight), float(eps), _ptr(positions), f32, naxes, counts, pairs,
+            _ptr(inv_freq), int(bool(interleaved)), float(rope_scale), _ptr(outs[0]),
+            _ptr(outs[1]), _ptr(outs[2]), _stream_of(dev, stream))
+    _check("spark_qk_norm_rope", st)
+    return tuple(outs)
+
+
+def spark_attend_ranges(nq, q_offsets, k_offsets=None, c_offsets=None, prefix=None, causal=False,
+                        ranges=None, err=None, stream=None):
+    """Key ranges [nq, 4] int32 of packed segments' query rows, from int32 offsets [segments + 1]
+    of their queries, video keys and context keys; causal ends a row's context range behind its
+    own place or the segment's prefix."""
+    _need(q_offsets, "q_offsets", torch.int32)
+    dev, n = q_offsets.device, q_offsets.numel()
+    for name, t, size in (("k_offsets", k_offsets, n), ("c_offsets", c_offsets, n),
+                          ("prefix", prefix, n - 1)):
+        if t is not None:
+            _need(t, name, torch.int32, dev)
+            if t.numel() != size:
+                raise ValueError(f"{name} must hold {size} values")
+    if prefix is not None and not causal:
+        raise ValueError("prefix needs causal")
+    if ranges is None:
+        ranges = torch.empty(max(int(nq), 0), 4, dtype=torch.int32, device=dev)
+    _need(ranges, "ranges", torch.int32, dev)
+    if ranges.shape != (nq, 4):
+        raise ValueError("ranges must have the shape [nq, 4]")
+    with _on(dev):
+        st = lib().spark_attend_ranges(int(nq), n - 1, _ptr(q_offsets), _ptr(k_offsets),
+                                       _ptr(c_offsets), _ptr(prefix), int(bool(causal)),
+                                       _ptr(ranges), _ptr(err), _stream_of(dev, stream))
+    _check("spark_attend_ranges", st)
+    return ranges
+
+
+def spark_attend_dense_workspace_size(H, nq, nk, nc, d) -> int:
+    return int(lib().spark_attend_dense_workspace_size(H, nq, nk, nc, d))
+
+
+def spark_attend_dense(Q, K, V, Kc=None, Vc=None, ranges=None, out_dtype=torch.bfloat16, out=None,
+                       lse=None, workspace=None, err=None, stream=None):
+    """Dense attention of the rows of Q [H, nq, d] over the video keys K, V [H, nk, d] and the
+    context keys Kc, Vc [H, nc, d] (bf16), each row over its ranges ([nq, 4] int32, None: all);
+    returns (out, lse)."""
+    bf = torch.bfloat16
+    _need(Q, "Q", bf)
+    dev = Q.device
+    if Q.dim() != 3:
+        raise ValueError("Q must have the shape [H, nq, d]")
+    H, nq, d = Q.shape
+    for name, t in (("K", K), ("V", V)):
+        _need(t, name, bf, dev)
+    if K.dim() != 3 or K.shape[0] != H or K.shape[2] != d or V.shape != K.shape:
+        raise ValueError("K and V must have the shape [H, nk, d]")
+    Kc, Vc, nc = _context_args(Kc, Vc, H, d, bf, dev)
+    nk = K.shape[1]
+    if ranges is not None:
+        _need(ranges, "ranges", torch.int32, dev)
+        if ranges.shape != (nq, 4):
+            raise ValueError("ranges must have the shape [nq, 4]")
+    if out is None:
+        out = torch.empty(H, nq, d, dtype=out_dtype, device=dev)
+    _need(out, "out", (bf, torch.float32), dev)
+    if lse is None:
+        lse = torch.empty(H, nq, dtype=torch.float32, device=dev)
+    _need(lse, "lse", torch.float32, dev)
+    if out.shape != Q.shape or lse.shape != (H, nq):
+        raise ValueError("out and lse must have the shapes [H, nq, d] and [H, nq]")
+    if workspace is None:
+        workspace = torch.empty(spark_attend_dense_workspace_size(H, nq, nk, nc, d),
+                                dtype=torch.uint8, device=dev)
+    _need(workspace, "workspace", torch.uint8, dev)
+    if err is not None:
+        _need(err, "err", torch.int32, dev)
+    with _on(dev):
+        st = lib().spark_attend_dense(_ptr(Q), _ptr(K), _ptr(V), _ptr(Kc), _ptr(Vc), H, nq, nk,
+                                      nc, d, _ptr(ranges), _ptr(out), _code(out.dtype), _ptr(lse),
+                                      _ptr(workspace), workspace.numel(), _ptr(err),
+                                      _stream_of(dev, stream))
+    _check("spark_attend_dense", st)
+    return out, lse
+
+
+def spark_bsa_workspace_size_joint(H, N, d, nqb, nkb, topk_ratio, nc) -> int:
+    return int(lib().spark_bsa_workspace_size_joint(H, N, d, nqb, nkb, float(topk_ratio), nc))
+
+
+def spark_bsa_forward_joint(Q, K, V, Qc, Kc, Vc, q_perm, k_perm, q_offsets, k_offsets, topk_ratio,
+                            out=None, out_c=None, workspace=None, stream=None):
+    """spark_bsa_forward_ctx for the video queries and dense attention for the context queries
+    Qc [H, nc, d]; returns (out, out_c, workspace, layout)."""
+    _need(Q, "Q", (torch.bfloat16, torch.float32))
+    dev = Q.device
+    H, N, d = Q.shape
+    for n, t in (("K", K), ("V", V), ("Qc", Qc)):
+        _need(t, n, Q.dtype, dev)
+    if K.shape != Q.shape or V.shape != Q.shape:
+        raise ValueError("Q, K, V must share the shape [H, N, d]")
+    _need(Kc, "Kc", Q.dtype, dev)
+    Kc, Vc, nc = _context_args(Kc, Vc, H, d, Q.dtype, dev)
+    if Qc.shape != Kc.shape:
+        raise ValueError("Qc, Kc and Vc must share the shape [H, nc, d]")
+    for n, t in (("q_perm", q_perm), ("k_perm", k_perm)):
+        _need(t, n, torch.int32, dev)
+        if t.shape != (H, N):
+            raise ValueError(f"{n} must have shape [H, N]")
+    for n, t in (("q_offsets", q_offsets), ("k_offsets", k_offsets)):
+        _need(t, n, torch.int32, dev)
+    nqb, nkb = q_offsets.numel() - 1, k_offsets.numel() - 1
+    layout = spark_bsa_workspace_layout(H, N, d, nqb, nkb, topk_ratio)
+    if out is None:
+        out = torch.empty_like(Q)
+    if out_c is None:
+        out_c = torch.empty_like(Qc)
+    _need(out, "out", Q.dtype, dev)
+    _need(out_c, "out_c", Q.dtype, dev)
+    if out.shape != Q.shape or out_c.shape != Qc.shape:
+        raise ValueError("out and out_c must have the shapes of Q and Qc")
+    if workspace is None:
+        size = spark_bsa_workspace_size_joint(H, N, d, nqb, nkb, topk_ratio, nc)
+        workspace = torch.empty(size, dtype=torch.uint8, device=dev)
+    _need(workspace, "workspace", torch.uint8, dev)
+    with _on(dev):
+        st = lib().spark_bsa_forward_joint(
+            _ptr(Q), _ptr(K), _ptr(V), _ptr(Qc), _ptr(Kc), _ptr(Vc), nc, _code(Q.dtype), H, N, d,
+            _ptr(q_perm), _ptr(k_perm), _ptr(q_offsets), nqb, _ptr(k_offsets), nkb,
+            float(topk_ratio), _ptr(out), _ptr(out_c), _ptr(workspace), workspace.numel(),
+            _stream_of(dev, stream))
+    _check("spark_bsa_forward_joint", st)
+    return out, out_c, workspace, layout

@@ -21,7 +21,7 @@ BUILD_DIR = os.path.join(PKG_DIR, "_build")
 LIB_NAME = "libspark_bsa.so"
 LIB_PATH = os.path.join(PKG_DIR, LIB_NAME)
 SOURCES = ["api.cu", "gather.cu", "route.cu", "attention.cu", "noalloc.cu", "reblock.cu",
-           "quant.cu"]
+           "quant.cu", "dense.cu", "rope.cu"]
 HEADERS = ["spark_ptx.cuh", "spark_kernels.cuh"]
 
 NVCC_FLAGS = [

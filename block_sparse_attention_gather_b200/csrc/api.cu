@@ -237,6 +237,31 @@ spark_status check_context(const void* Kc, const void* Vc, int nc) {
   return SPARK_OK;
 }
 
+spark_status check_dense(int H, int nq, int nk, int nc, int d) {
+  if (H < 1 || nq < 1 || nk < 0 || nc < 0) return SPARK_ERR_INVALID_ARG;
+  if (d != 64 && d != 128) return SPARK_ERR_UNSUPPORTED;
+  if (H > 65535 || nq > SPARK_MAX_DENSE || nk > SPARK_MAX_DENSE || nc > SPARK_MAX_NC)
+    return SPARK_ERR_UNSUPPORTED;
+  return SPARK_OK;
+}
+
+// Dense attention; arguments checked by the caller.
+spark_status dense_impl(const void* Q, const void* K, const void* V, const void* Kc,
+                        const void* Vc, int H, int nq, int nk, int nc, int d,
+                        const int32_t* ranges, void* out, int out_dtype, float* lse,
+                        void* workspace, uint32_t* err, cudaStream_t s) {
+  DenseMaps maps;
+  if (!encode_rows_map(&maps.q, Q, H, nq, d)) return SPARK_ERR_CUDA;
+  maps.k = maps.v = maps.kc = maps.vc = maps.q;  // an empty set has no tile to load
+  if (nk > 0 && (!encode_rows_map(&maps.k, K, H, nk, d) || !encode_rows_map(&maps.v, V, H, nk, d)))
+    return SPARK_ERR_CUDA;
+  if (nc > 0 &&
+      (!encode_rows_map(&maps.kc, Kc, H, nc, d) || !encode_rows_map(&maps.vc, Vc, H, nc, d)))
+    return SPARK_ERR_CUDA;
+  return from_cuda(launch_attend_dense(maps, H, nq, nk, nc, d, ranges, out, out_dtype, lse,
+                                       workspace, err, s));
+}
+
 // The whole forward pass; nc == 0 runs without context rows.
 spark_status forward_impl(const void* Q, const void* K, const void* V, const void* Kc,
                           const void* Vc, int nc, int dtype, int H, int N, int d,
@@ -965,6 +990,191 @@ spark_status spark_reblock(const void* Q, const void* K, int dtype, int H, int N
     return SPARK_ERR_CUDA;
   }
   return from_cuda(launch_reblock_offsets(offsets, L.nb, N, block, s));
+}
+
+// ------------------------------------------------------- norm and rotation of Q and K
+
+spark_status spark_qk_norm_rope(const void* Q, const void* K, const void* V, int dtype, int H,
+                                int N, int d, const int64_t* strides, const float* q_weight,
+                                const float* k_weight, double eps, const void* positions,
+                                int positions_f32, int naxes, const int32_t* axis_pairs,
+                                int pairs, const float* inv_freq, int interleaved,
+                                double rope_scale, void* Q_out, void* K_out, void* V_out,
+                                void* stream) {
+  if (!Q || !Q_out || (K && !K_out) || (V && !V_out)) return SPARK_ERR_INVALID_ARG;
+  if (dtype != SPARK_BF16 && dtype != SPARK_F32) return SPARK_ERR_INVALID_ARG;
+  if (H < 1 || N < 1) return SPARK_ERR_INVALID_ARG;
+  if (d != 64 && d != 128) return SPARK_ERR_UNSUPPORTED;
+  if (H > 65535) return SPARK_ERR_UNSUPPORTED;
+  if (!(eps >= 0.0) || !std::isfinite(eps) || !std::isfinite(rope_scale))
+    return SPARK_ERR_INVALID_ARG;
+  if (pairs < 0 || pairs > d / 2) return SPARK_ERR_INVALID_ARG;
+  RopeArgs a{};
+  const void* in[3] = {Q, K, V};
+  void* out[3] = {Q_out, K_out, V_out};
+  const size_t esize = dtype == SPARK_BF16 ? 2 : 4;
+  for (int t = 0; t < 3; ++t) {
+    a.in[t] = in[t];
+    a.out[t] = in[t] ? out[t] : nullptr;
+    a.head_stride[t] = strides ? strides[2 * t] : static_cast<long long>(N) * d;
+    a.token_stride[t] = strides ? strides[2 * t + 1] : d;
+    if (!in[t]) continue;
+    if (!aligned(in[t], esize) || !aligned(out[t], esize)) return SPARK_ERR_INVALID_ARG;
+    // in place: every row is read and written by the same threads, at the same place
+    if (in[t] == out[t] && !((H == 1 || a.head_stride[t] == static_cast<long long>(N) * d) &&
+                             (N == 1 || a.token_stride[t] == d)))
+      return SPARK_ERR_INVALID_ARG;
+  }
+  a.weight[0] = q_weight;
+  a.weight[1] = k_weight;
+  a.eps = static_cast<float>(eps);
+  a.scale = static_cast<float>(rope_scale);
+  a.H = H;
+  a.N = N;
+  a.pairs = pairs;
+  a.naxes = 1;
+  if (pairs > 0) {
+    if (!positions || !inv_freq || !axis_pairs || naxes < 1) return SPARK_ERR_INVALID_ARG;
+    if (naxes > SPARK_MAX_ROPE_AXES) return SPARK_ERR_UNSUPPORTED;
+    long long sum = 0;
+    for (int k = 0; k < naxes; ++k) {
+      if (axis_pairs[k] < 0) return SPARK_ERR_INVALID_ARG;
+      a.first[k] = static_cast<int>(sum);
+      sum += axis_pairs[k];
+      if (sum > pairs) return SPARK_ERR_INVALID_ARG;
+    }
+    if (sum != pairs) return SPARK_ERR_INVALID_ARG;
+    a.first[naxes] = pairs;
+    a.naxes = naxes;
+    a.positions = positions;
+    a.positions_f32 = positions_f32 != 0;
+    a.inv_freq = inv_freq;
+    a.interleaved = interleaved != 0;
+  }
+  return from_cuda(launch_qk_norm_rope(a, dtype, d, as_stream(stream)));
+}
+
+spark_status spark_rope_frequencies(const int32_t* axis_pairs, int naxes, double base,
+                                    int scaling, double factor, double original, float* inv_freq,
+                                    double* rope_scale) {
+  if (!axis_pairs || !inv_freq || !rope_scale || naxes < 1) return SPARK_ERR_INVALID_ARG;
+  if (naxes > SPARK_MAX_ROPE_AXES) return SPARK_ERR_UNSUPPORTED;
+  if (!(base > 1.0) || !std::isfinite(base)) return SPARK_ERR_INVALID_ARG;
+  if (scaling < SPARK_ROPE_NONE || scaling > SPARK_ROPE_YARN) return SPARK_ERR_INVALID_ARG;
+  if (scaling != SPARK_ROPE_NONE && (!(factor >= 1.0) || !std::isfinite(factor)))
+    return SPARK_ERR_INVALID_ARG;
+  if (scaling == SPARK_ROPE_YARN && (!(original > 0.0) || !std::isfinite(original)))
+    return SPARK_ERR_INVALID_ARG;
+  for (int k = 0; k < naxes; ++k)
+    if (axis_pairs[k] < 0) return SPARK_ERR_INVALID_ARG;
+  constexpr double kTwoPi = 6.283185307179586;
+  for (int k = 0; k < naxes; ++k) {
+    const int n = axis_pairs[k];
+    const double b =
+        scaling == SPARK_ROPE_NTK && n > 1 ? base * std::pow(factor, n / (n - 1.0)) : base;
+    // YaRN: index of the pair that turns `turns` times over the original positions
+    auto index = [&](double turns) {
+      return n * std::log(original / (turns * kTwoPi)) / std::log(base);
+    };
+    double lo = 0.0, hi = 1.0;
+    if (scaling == SPARK_ROPE_YARN) {
+      lo = std::fmax(std::floor(index(32.0)), 0.0);
+      hi = std::fmin(std::ceil(index(1.0)), 2.0 * n - 1.0);
+      if (hi <= lo) hi = lo + 0.001;                     // a step, no ramp
+    }
+    for (int i = 0; i < n; ++i) {
+      double f = std::pow(b, -static_cast<double>(i) / n);
+      if (scaling == SPARK_ROPE_LINEAR) f /= factor;
+      if (scaling == SPARK_ROPE_YARN) {
+        const double r = std::fmin(std::fmax((i - lo) / (hi - lo), 0.0), 1.0);
+        f = f / factor * r + f * (1.0 - r);
+      }
+      *inv_freq++ = static_cast<float>(f);
+    }
+  }
+  *rope_scale = scaling == SPARK_ROPE_YARN ? 0.1 * std::log(factor) + 1.0 : 1.0;
+  return SPARK_OK;
+}
+
+// ------------------------------------------------------------------- dense attention
+
+size_t spark_attend_dense_workspace_size(int H, int nq, int nk, int nc, int d) {
+  return check_dense(H, nq, nk, nc, d) == SPARK_OK ? attend_dense_workspace(H, nq, nk, nc, d) : 0;
+}
+
+spark_status spark_attend_dense(const void* Q, const void* K, const void* V, const void* Kc,
+                                const void* Vc, int H, int nq, int nk, int nc, int d,
+                                const int32_t* ranges, void* out, int out_dtype, float* lse,
+                                void* workspace, size_t workspace_bytes, uint32_t* err,
+                                void* stream) {
+  spark_status st = check_dense(H, nq, nk, nc, d);
+  if (st != SPARK_OK) return st;
+  if (!Q || !out || (nk > 0 && (!K || !V)) || (nc > 0 && (!Kc || !Vc)))
+    return SPARK_ERR_INVALID_ARG;
+  if (out_dtype != SPARK_BF16 && out_dtype != SPARK_F32) return SPARK_ERR_INVALID_ARG;
+  if (!aligned(Q, 16) || !aligned(out, 16) || !aligned(ranges, 16) || !aligned(lse, 4) ||
+      (nk > 0 && (!aligned(K, 16) || !aligned(V, 16))) ||
+      (nc > 0 && (!aligned(Kc, 16) || !aligned(Vc, 16))))
+    return SPARK_ERR_INVALID_ARG;
+  if (!workspace || workspace_bytes < attend_dense_workspace(H, nq, nk, nc, d) ||
+      !aligned(workspace, kAlign))
+    return SPARK_ERR_WORKSPACE;
+  return dense_impl(Q, K, V, Kc, Vc, H, nq, nk, nc, d, ranges, out, out_dtype, lse, workspace, err,
+                    as_stream(stream));
+}
+
+spark_status spark_attend_ranges(int nq, int nseg, const int32_t* q_offsets,
+                                 const int32_t* k_offsets, const int32_t* c_offsets,
+                                 const int32_t* prefix, int causal, int32_t* ranges,
+                                 uint32_t* err, void* stream) {
+  if (!q_offsets || !ranges || nq < 1 || nseg < 1) return SPARK_ERR_INVALID_ARG;
+  if (nq > SPARK_MAX_DENSE || nseg > SPARK_MAX_DENSE) return SPARK_ERR_UNSUPPORTED;
+  if (!aligned(ranges, 16)) return SPARK_ERR_INVALID_ARG;
+  return from_cuda(launch_attend_ranges(nq, nseg, q_offsets, k_offsets, c_offsets, prefix,
+                                        causal != 0, ranges, err, as_stream(stream)));
+}
+
+size_t spark_bsa_workspace_size_joint(int H, int N, int d, int nqb, int nkb, double topk_ratio,
+                                      int nc) {
+  const size_t base = spark_bsa_workspace_size_ctx(H, N, d, nqb, nkb, topk_ratio, nc);
+  if (base == 0 || nc < 1 || check_dense(H, nc, N, nc, d) != SPARK_OK) return 0;
+  return base + context_bytes(H, nc, d) + attend_dense_workspace(H, nc, N, nc, d);
+}
+
+spark_status spark_bsa_forward_joint(const void* Q, const void* K, const void* V, const void* Qc,
+                                     const void* Kc, const void* Vc, int nc, int dtype, int H,
+                                     int N, int d, const int32_t* q_perm, const int32_t* k_perm,
+                                     const int32_t* q_block_offsets, int nqb,
+                                     const int32_t* k_block_offsets, int nkb, double topk_ratio,
+                                     void* out, void* out_c, void* workspace,
+                                     size_t workspace_bytes, void* stream) {
+  if (!Qc || !out_c || nc < 1 || !aligned(Qc, 16) || !aligned(out_c, 16))
+    return SPARK_ERR_INVALID_ARG;
+  spark_bsa_layout L;
+  spark_status st = layout_of(H, N, d, nqb, nkb, topk_ratio, &L);
+  if (st == SPARK_OK) st = check_context(Kc, Vc, nc);
+  if (st == SPARK_OK) st = check_dense(H, nc, N, nc, d);
+  if (st != SPARK_OK) return st;
+  const size_t cbytes = context_bytes(H, nc, d);
+  const size_t base = L.total + 2 * cbytes;
+  if (!workspace || !aligned(workspace, kAlign) ||
+      workspace_bytes < base + cbytes + attend_dense_workspace(H, nc, N, nc, d))
+    return SPARK_ERR_WORKSPACE;
+  cudaStream_t s = as_stream(stream);
+  st = forward_impl(Q, K, V, Kc, Vc, nc, dtype, H, N, d, q_perm, k_perm, q_block_offsets, nqb,
+                    k_block_offsets, nkb, topk_ratio, out, workspace, base, s);
+  if (st != SPARK_OK) return st;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  const void* Qb = Qc;
+  if (dtype == SPARK_F32) {                      // Kc, Vc were converted behind the layout
+    if (launch_to_bf16(Qc, dtype, static_cast<size_t>(H) * nc * d, ws + base, s) != cudaSuccess)
+      return SPARK_ERR_CUDA;
+    Qb = ws + base;
+    Kc = ws + L.total;
+    Vc = ws + L.total + cbytes;
+  }
+  return dense_impl(Qb, ws + L.Kp, ws + L.Vp, Kc, Vc, H, nc, N, nc, d, nullptr, out_c, dtype,
+                    nullptr, ws + base + cbytes, reinterpret_cast<uint32_t*>(ws + L.err), s);
 }
 
 }  // extern "C"

@@ -1,0 +1,664 @@
+// Dense attention of query rows over the video keys and the context keys (tcgen05 + TMEM + TMA),
+// and the key ranges it reads.
+//
+// Spark-H3 blog, section "Spark-Reblock": context/sink tokens stay exact.  Their own queries
+// attend every video and context key; the same blog's runs keep the first layer and the warm-up
+// steps dense.  Per head h and query row i, over the keys j of the row's two ranges,
+//   s_j = sigma q_i . k_j,   out_i = sum_j exp(s_j - lse_i) v_j,   lse_i = log sum_j exp(s_j).
+//
+// One pass over the keys with a running reference per row (an online softmax):
+//   p_j = 2^(s_j log2e - ref),  l = sum p,  O = sum p v,  out = O / l,  lse = (ref + log2 l) ln2.
+// ref starts as the row's maximum over its first tile with a live key and follows the running
+// maximum only when that exceeds ref by more than 2^8 (then O and l are rescaled): between
+// rescales p stays under 2^8 and its rounding to bf16 for the tensor cores is relative, so a
+// reference below the true maximum costs no accuracy.  l and O are fp32.
+//
+// One CTA works on one head, one slice of the key tiles, and
+//   kPair:  two 128-row query tiles, one per softmax group; every K and V tile serves both;
+//   !kPair: one 128-row query tile; the groups take the even and the odd key tiles, each with
+//           its own O, and the epilogue joins them.
+// 10 warps: 0-3 / 4-7 the softmax groups (warp w owns TMEM lanes 32*(w%4)..), 8 the TMA
+// producer, 9 the MMA issuer.  TMEM columns: S_g at 128 g (P_g written over it as bf16), O_g at
+// 256 + D g.  The next S of a group is issued behind the PV that reads its P, so the commit that
+// announces S(t+1) also tells that PV(t) is complete and O may be rescaled.
+//
+// Keys beyond a row's ranges are masked to -inf by value, so what they hold (NaN included) does
+// not matter; rows of V outside the ranges of the whole query tile pair are zeroed in shared
+// memory before the product, as 0 * NaN would not be 0.
+//
+// Every wait is bounded (see spark_ptx.cuh); on expiry the kernel flags kErrTimeout, drains its
+// copies and MMAs, frees TMEM and returns.
+#include <climits>
+
+#include "spark_kernels.cuh"
+
+namespace spark {
+
+namespace {
+
+constexpr int kWarpLoad = 8, kWarpMma = 9;
+constexpr int kThreads = 320;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kLag = 8.f;                  // log2 units the reference may lag the maximum by
+constexpr int kMaxSplits = 64;
+
+template <int D, bool kPair>
+struct Cfg {
+  static constexpr int kTile = 128 * D * 2;                  // bytes of one Q, K or V tile
+  static constexpr int kQTiles = kPair ? 2 : 1;
+  // what 227 KB hold next to the query tiles (d = 64: as deep as d = 128 in bytes)
+  static constexpr int kStages = (D == 128 ? 1 : 2) * (kPair ? 5 : 6);
+  static constexpr size_t kSmem = 1024 + static_cast<size_t>(kQTiles + kStages) * kTile;
+};
+
+template <int kStages>
+struct __align__(8) Bars {
+  uint64_t qfull, full[kStages], empty[kStages], sfull[2], pready[2], done;
+  uint32_t tmem;
+  int abort_flag;
+};
+
+// The key tiles of a CTA: the hull of its rows' video range, then of their context range, each
+// cut into tiles of 128 rows from its own start.
+struct Tiles {
+  int vb, ve, cb, ce;      // hulls
+  int tv;                  // video tiles
+  int first, count;        // this CTA's slice of them all
+
+  __device__ __forceinline__ bool video(int t) const { return first + t < tv; }
+  __device__ __forceinline__ int row(int t) const {
+    const int a = first + t;
+    return a < tv ? vb + a * 128 : cb + (a - tv) * 128;
+  }
+};
+
+__device__ __forceinline__ bool drain(uint64_t* bar, uint32_t parity) {
+  const uint64_t t0 = globaltimer_ns();
+  while (!mbar_test(bar, parity)) {
+    if (globaltimer_ns() - t0 > kWaitLimitNs) return false;
+  }
+  return true;
+}
+
+// Order of the tiles in the shared-memory ring: the order in which the MMA warp first uses them.
+//   kPair:  K0 V0 K1 V1 ...;   otherwise  K0 K1 V0 K2 V1 ... K(T-1) V(T-2) V(T-1).
+template <bool kPair>
+__device__ __forceinline__ int slot_k(int t) {
+  return kPair ? 2 * t : max(2 * t - 1, 0);
+}
+template <bool kPair>
+__device__ __forceinline__ int slot_v(int t, int T) {
+  return kPair ? 2 * t + 1 : min(2 * t + 2, 2 * T - 1);
+}
+
+__device__ __forceinline__ float max128(const float (&x)[128]) {
+  float mx[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+  for (int j = 4; j < 124; j += 8) {
+    mx[0] = fmax3(mx[0], x[j], x[j + 1]);
+    mx[1] = fmax3(mx[1], x[j + 2], x[j + 3]);
+    mx[2] = fmax3(mx[2], x[j + 4], x[j + 5]);
+    mx[3] = fmax3(mx[3], x[j + 6], x[j + 7]);
+  }
+  mx[0] = fmax3(mx[0], x[124], x[125]);
+  mx[1] = fmax3(mx[1], x[126], x[127]);
+  return fmaxf(fmax3(mx[0], mx[1], mx[2]), mx[3]);
+}
+
+}  // namespace
+
+template <int D, bool kPair>
+__global__ void __launch_bounds__(kThreads, 1) attend_dense_kernel(
+    const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
+    const __grid_constant__ CUtensorMap map_v, const __grid_constant__ CUtensorMap map_kc,
+    const __grid_constant__ CUtensorMap map_vc, int nq, int nk, int nc,
+    const int4* __restrict__ ranges, int nsplit, void* __restrict__ out, int out_dtype,
+    float* __restrict__ lse, float* __restrict__ part, float2* __restrict__ part_ml,
+    uint32_t* err, uint64_t wait_ns) {
+  using C = Cfg<D, kPair>;
+  constexpr int kStages = C::kStages;
+  constexpr int kAtoms = D / 64;
+  constexpr uint32_t kAll = 0xffffffffu;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint8_t* qst = smem;
+  uint8_t* ring = qst + C::kQTiles * C::kTile;
+  __shared__ Bars<kStages> bars;
+  __shared__ int s_skip;
+  __shared__ int hull[8][4];
+  // [group][row] references and sums, over the query tile once every MMA has read it
+  float(*ex_m)[128] = reinterpret_cast<float(*)[128]>(qst);
+  float(*ex_l)[128] = reinterpret_cast<float(*)[128]>(qst + 1024);
+  volatile int* abort_flag = &bars.abort_flag;
+
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+  const int h = blockIdx.z, split = blockIdx.y;
+  const int q0 = blockIdx.x * (kPair ? 256 : 128);
+  const int groups = kPair && q0 + 128 < nq ? 2 : 1;      // query tiles with rows (kPair)
+
+  // This thread's row and its key ranges; rows past nq count as unmasked and are never stored.
+  const int grp = (warp >> 2) & 1, q4 = warp & 3;
+  const int row = q4 * 32 + lane;
+  const int qi = q0 + (kPair ? grp * 128 : 0) + row;
+  const bool live = warp < 8 && qi < nq;
+  int4 rg = make_int4(0, INT_MAX, 0, INT_MAX);
+  if (warp < 8) {
+    int4 r = make_int4(INT_MAX, 0, INT_MAX, 0);
+    if (live) {
+      if (ranges != nullptr) rg = ranges[qi];
+      rg.x = max(rg.x, 0), rg.y = min(rg.y, nk);
+      rg.z = max(rg.z, 0), rg.w = min(rg.w, nc);
+      if (rg.x < rg.y) r.x = rg.x, r.y = rg.y;
+      if (rg.z < rg.w) r.z = rg.z, r.w = rg.w;
+    }
+    const int a = __reduce_min_sync(kAll, r.x), b = __reduce_max_sync(kAll, r.y);
+    const int c = __reduce_min_sync(kAll, r.z), e = __reduce_max_sync(kAll, r.w);
+    if (lane == 0) hull[warp][0] = a, hull[warp][1] = b, hull[warp][2] = c, hull[warp][3] = e;
+  }
+  if (tid == 0) {
+    s_skip = launch_timed_out(err) ? 1 : 0;               // an earlier CTA gave up
+    bars.abort_flag = 0;
+    mbar_init(&bars.qfull, 1);
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&bars.full[s], 1);
+      mbar_init(&bars.empty[s], 1);
+    }
+    for (int g = 0; g < 2; ++g) {
+      mbar_init(&bars.sfull[g], 1);
+      mbar_init(&bars.pready[g], 128);
+    }
+    mbar_init(&bars.done, 1);
+    mbar_fence_init();
+  }
+  if (warp == kWarpMma) {
+    tmem_alloc(&bars.tmem, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tbase = bars.tmem;
+  if (s_skip) {                                            // uniform: give back TMEM and leave
+    if (warp == kWarpMma) tmem_dealloc(tbase, 512);
+    return;
+  }
+  Tiles tl{INT_MAX, 0, INT_MAX, 0, 0, 0, 0};
+#pragma unroll
+  for (int w = 0; w < 8; ++w) {
+    tl.vb = min(tl.vb, hull[w][0]), tl.ve = max(tl.ve, hull[w][1]);
+    tl.cb = min(tl.cb, hull[w][2]), tl.ce = max(tl.ce, hull[w][3]);
+  }
+  {
+    tl.tv = tl.ve > tl.vb ? (tl.ve - tl.vb + 127) / 128 : 0;
+    const long long n = tl.tv + (tl.ce > tl.cb ? (tl.ce - tl.cb + 127) / 128 : 0);
+    tl.first = static_cast<int>(n * split / nsplit);
+    tl.count = static_cast<int>(n * (split + 1) / nsplit) - tl.first;
+  }
+  const int T = tl.count;
+
+  if (warp == kWarpLoad) {
+    // -------------------------------------------------------------------- TMA producer
+    int issued = 0;
+    if (T > 0) {
+      if (elect_one()) {
+        tma_prefetch_desc(&map_k);
+        tma_prefetch_desc(&map_v);
+        mbar_arrive_expect_tx(&bars.qfull, groups * C::kTile);
+        for (int g = 0; g < groups; ++g)
+          for (int a = 0; a < kAtoms; ++a)
+            tma_load_3d(qst + g * C::kTile + a * 16384, &map_q, &bars.qfull, a * 64,
+                        q0 + g * 128, h);
+      }
+      __syncwarp();
+      int nk_done = 0, nv_done = 0;                        // K and V tiles issued
+      for (int i = 0; i < 2 * T; ++i) {
+        const bool is_k = nk_done < T && slot_k<kPair>(nk_done) == i;
+        const int t = is_k ? nk_done++ : nv_done++;
+        const int s = i % kStages;
+        if (i >= kStages &&
+            !__all_sync(kAll, mbar_wait(&bars.empty[s], ((i / kStages) - 1) & 1, abort_flag, err,
+                                        wait_ns)))
+          break;
+        if (elect_one()) {
+          mbar_arrive_expect_tx(&bars.full[s], C::kTile);
+          const CUtensorMap* m = tl.video(t) ? (is_k ? &map_k : &map_v)
+                                             : (is_k ? &map_kc : &map_vc);
+          for (int a = 0; a < kAtoms; ++a)
+            tma_load_3d(ring + s * C::kTile + a * 16384, m, &bars.full[s], a * 64, tl.row(t), h);
+        }
+        __syncwarp();
+        issued = i + 1;
+      }
+      // every load has landed before the CTA ends (after an abort some were never consumed)
+      for (int i = max(0, issued - kStages); i < issued; ++i)
+        drain(&bars.full[i % kStages], (i / kStages) & 1);
+      drain(&bars.qfull, 0);
+    }
+  } else if (warp == kWarpMma) {
+    // ---------------------------------------------------------------------- MMA issuer
+    constexpr uint32_t idS = idesc_bf16(128, 128, false, false);
+    constexpr uint32_t idO = idesc_bf16(128, D, false, true);
+    const uint64_t qd = sdesc_sw128(smem_u32(qst), 16, 1024);
+    const uint64_t kd0 = sdesc_sw128(smem_u32(ring), 16, 1024);
+    const uint64_t vd0 = sdesc_sw128(smem_u32(ring), 16384, 1024);
+    bool ok = T > 0 && __all_sync(kAll, mbar_wait(&bars.qfull, 0, abort_flag, err, wait_ns));
+    auto wait_full = [&](int i) {
+      return __all_sync(kAll, mbar_wait(&bars.full[i % kStages], (i / kStages) & 1, abort_flag,
+                                        err, wait_ns));
+    };
+    // S of key tile t into group g's buffer; the last reader of the K tile frees its stage
+    auto issue_s = [&](int t, int g, bool last) -> bool {
+      const int i = slot_k<kPair>(t);
+      if (!wait_full(i)) return false;
+      const uint64_t kd = kd0 + static_cast<uint64_t>((i % kStages) * (C::kTile >> 4));
+      const uint64_t q = qd + static_cast<uint64_t>(kPair ? g * (C::kTile >> 4) : 0);
+      if (elect_one()) {
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t off = ((kk / 4) * 16384 + (kk % 4) * 32) / 16;
+          mma_ss(tbase + g * 128, q + off, kd + off, idS, kk > 0 ? 1u : 0u);
+        }
+        tc_commit(&bars.sfull[g]);
+        if (last) tc_commit(&bars.empty[i % kStages]);
+      }
+      __syncwarp();
+      return true;
+    };
+    // O_g += P V of key tile t (the n-th tile of the group)
+    auto issue_pv = [&](int t, int g, int n, bool last) -> bool {
+      if (!__all_sync(kAll, mbar_wait(&bars.pready[g], n & 1, abort_flag, err, wait_ns)))
+        return false;
+      tc_fence_after_sync();
+      const int i = slot_v<kPair>(t, T);
+      if (!wait_full(i)) return false;
+      const uint64_t vd = vd0 + static_cast<uint64_t>((i % kStages) * (C::kTile >> 4));
+      if (elect_one()) {
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)
+          mma_ts(tbase + 256 + g * D, tbase + g * 128 + kk * 8, vd + (kk * 2048) / 16, idO,
+                 (kk > 0 || n > 0) ? 1u : 0u);
+        if (last) tc_commit(&bars.empty[i % kStages]);
+      }
+      __syncwarp();
+      return true;
+    };
+    if constexpr (kPair) {
+      for (int g = 0; ok && g < groups; ++g) ok = issue_s(0, g, g + 1 == groups);
+      for (int t = 0; ok && t < T; ++t)
+        for (int g = 0; ok && g < groups; ++g) {
+          ok = issue_pv(t, g, t, g + 1 == groups);
+          if (ok && t + 1 < T) ok = issue_s(t + 1, g, g + 1 == groups);
+        }
+    } else {
+      for (int t = 0; ok && t < min(T, 2); ++t) ok = issue_s(t, t, true);
+      for (int t = 0; ok && t < T; ++t) {
+        ok = issue_pv(t, t & 1, t >> 1, true);
+        if (ok && t + 2 < T) ok = issue_s(t + 2, t & 1, true);
+      }
+    }
+    // every MMA complete: the epilogue reads O, and TMEM is freed after
+    if (elect_one()) tc_commit(&bars.done);
+    __syncwarp();
+    drain(&bars.done, 0);
+  } else {
+    // -------------------------------------------------------------------- softmax rows
+    const uint32_t lane_off = static_cast<uint32_t>(q4 * 32) << 16;
+    const uint32_t sbuf = tbase + lane_off + grp * 128;
+    const uint32_t obuf = tbase + lane_off + 256 + grp * D;
+    const float c = kLog2e * rsqrtf(static_cast<float>(D));
+    const bool warp_live = __any_sync(kAll, live);         // else nothing of this warp is stored
+    float ref = -INFINITY, l = 0.f;                        // log2 units; sum of 2^(. - ref)
+    const int ntiles = kPair ? (grp < groups ? T : 0) : (T + 1 - grp) / 2;
+    bool ok = true;
+    for (int n = 0; n < ntiles; ++n) {
+      const int t = kPair ? n : 2 * n + grp;
+      ok = __all_sync(kAll, mbar_wait(&bars.sfull[grp], n & 1, abort_flag, err, wait_ns));
+      if (!ok) break;
+      tc_fence_after_sync();
+      const int y = tl.row(t);
+      const bool video = tl.video(t);
+      if (warp_live) {
+        float x[128];
+        {
+          uint32_t r[64];
+          tmem_ld64(sbuf, r);
+#pragma unroll
+          for (int j = 0; j < 64; ++j) x[j] = __uint_as_float(r[j]);
+          tmem_ld64(sbuf + 64, r);
+#pragma unroll
+          for (int j = 0; j < 64; ++j) x[64 + j] = __uint_as_float(r[j]);
+        }
+        const int lo = max((video ? rg.x : rg.z) - y, 0);
+        const int hi = min((video ? rg.y : rg.w) - y, 128);
+        if (__any_sync(kAll, lo > 0 || hi < 128)) {
+          const unsigned width = static_cast<unsigned>(max(hi - lo, 0));
+#pragma unroll
+          for (int j = 0; j < 128; ++j)
+            if (static_cast<unsigned>(j - lo) >= width) x[j] = -INFINITY;
+        }
+        const float mx = max128(x) * c;
+        const bool grow = mx > ref + kLag;
+        if (__any_sync(kAll, grow)) {
+          const float next = grow ? mx : ref;
+          const float f = grow ? ex2_approx(ref - next) : 1.f;
+          ref = next;
+          l *= f;
+          if (n > 0) {
+#pragma unroll
+            for (int cc = 0; cc < D; cc += 32) {
+              uint32_t o[32];
+              tmem_ld32(obuf + cc, o);
+              uint32_t o2[16];
+#pragma unroll
+              for (int hh = 0; hh < 2; ++hh) {
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+                  o2[j] = __float_as_uint(__uint_as_float(o[hh * 16 + j]) * f);
+                tmem_st16_issue(obuf + cc + hh * 16, o2);
+              }
+            }
+          }
+        }
+        const float m = ref > -INFINITY ? ref : 0.f;       // no live key yet: every p is 0
+        const uint64_t c2 = f2_splat(c), nm2 = f2_splat(-m);
+        uint64_t sum2[2] = {0, 0};
+#pragma unroll
+        for (int cc = 0; cc < 128; cc += 32) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            const uint64_t a2 = f2_fma(f2_pack(x[cc + 2 * j], x[cc + 2 * j + 1]), c2, nm2);
+            float a0, a1;
+            f2_unpack(a2, a0, a1);
+            const float p0 = ex2_approx(a0), p1 = ex2_approx(a1);
+            sum2[j & 1] = f2_add(sum2[j & 1], f2_pack(p0, p1));
+            pk[j] = pack_bf16(p0, p1);
+          }
+          tmem_st16_issue(sbuf + cc / 2, pk);
+        }
+        float s0, s1;
+        f2_unpack(f2_add(sum2[0], sum2[1]), s0, s1);
+        l += s0 + s1;
+        tmem_wait_st();
+      }
+      // V rows past the hull that are not past the tensor (those TMA fills with zeros): zeroed
+      // by group 0, whose P the MMA warp waits for first (kPair), or by the tile's own group
+      const int end = video ? tl.ve : tl.ce, rows = video ? nk : nc;
+      if (y + 128 > end && end < rows && (!kPair || grp == 0)) {
+        const int i = slot_v<kPair>(t, T);
+        ok = __all_sync(kAll, mbar_wait(&bars.full[i % kStages], (i / kStages) & 1, abort_flag,
+                                        err, wait_ns));
+        if (!ok) break;
+        uint8_t* v = ring + (i % kStages) * C::kTile;
+        for (int a = 0; a < kAtoms; ++a)
+          for (int k = (end - y) * 8 + row; k < 128 * 8; k += 128)
+            *reinterpret_cast<uint4*>(v + a * 16384 + k * 16) = make_uint4(0, 0, 0, 0);
+        fence_proxy_async_smem();
+      }
+      tc_fence_before_sync();
+      mbar_arrive(&bars.pready[grp]);
+    }
+    // ---- epilogue
+    if (ok && T > 0)
+      ok = __all_sync(kAll, mbar_wait(&bars.done, 0, abort_flag, err, wait_ns));
+    float w[2] = {1.f, 1.f};                               // weights of the two groups' O
+    bool read0 = true, read1 = false;                      // which hold something
+    if constexpr (!kPair) {
+      ex_m[grp][row] = ref;
+      ex_l[grp][row] = l;
+      named_bar_sync(1 + q4, 64);                          // the two groups of this quarter
+      const float m0 = ex_m[0][row], m1 = ex_m[1][row];
+      ref = fmaxf(m0, m1);
+      w[0] = m0 > -INFINITY ? ex2_approx(m0 - ref) : 0.f;
+      w[1] = m1 > -INFINITY ? ex2_approx(m1 - ref) : 0.f;
+      l = w[0] * ex_l[0][row] + w[1] * ex_l[1][row];
+      read0 = T > 0, read1 = T > 1;
+    } else {
+      read0 = T > 0;
+    }
+    if (ok && warp_live && (kPair ? grp < groups : true)) {
+      tc_fence_after_sync();
+      const size_t at = static_cast<size_t>(h) * nq + qi;
+      const size_t prow = (static_cast<size_t>(h) * nsplit + split) * nq + qi;
+      // one slice: the output; several: unnormalised partial sums for the join
+      const float inv = nsplit > 1 ? 1.f : 1.f / l;
+      const bool none = l == 0.f;                          // no live key: zeros
+      constexpr int kCols = kPair ? D : D / 2;             // columns this warp stores
+      const int col0 = kPair ? 0 : grp * kCols;
+      const uint32_t o0 = tbase + lane_off + 256 + (kPair ? grp * D : 0);
+#pragma unroll
+      for (int cc = 0; cc < kCols; cc += 32) {
+        const int col = col0 + cc;
+        float o[32];
+#pragma unroll
+        for (int j = 0; j < 32; ++j) o[j] = 0.f;
+        if (read0) {
+          uint32_t a[32];
+          tmem_ld32(o0 + col, a);
+#pragma unroll
+          for (int j = 0; j < 32; ++j) o[j] = w[0] * __uint_as_float(a[j]);
+        }
+        if (read1) {
+          uint32_t a[32];
+          tmem_ld32(o0 + D + col, a);
+#pragma unroll
+          for (int j = 0; j < 32; ++j) o[j] = fmaf(w[1], __uint_as_float(a[j]), o[j]);
+        }
+        if (live) {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) o[j] = none ? 0.f : o[j] * inv;
+          if (nsplit > 1 || out_dtype == 1) {
+            float4* dst = reinterpret_cast<float4*>(
+                nsplit > 1 ? part + prow * D + col : static_cast<float*>(out) + at * D + col);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              dst[j] = make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+          } else {
+            uint4* dst =
+                reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(out) + at * D + col);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              dst[j] = make_uint4(pack_bf16(o[8 * j], o[8 * j + 1]),
+                                  pack_bf16(o[8 * j + 2], o[8 * j + 3]),
+                                  pack_bf16(o[8 * j + 4], o[8 * j + 5]),
+                                  pack_bf16(o[8 * j + 6], o[8 * j + 7]));
+          }
+        }
+      }
+      if (live && (kPair || grp == 0)) {
+        if (nsplit > 1)
+          part_ml[prow] = make_float2(ref, l);
+        else if (lse != nullptr)
+          lse[at] = (ref + log2f(l)) * kLn2;
+      }
+    }
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  if (warp == kWarpMma) {
+    tc_fence_after_sync();
+    tmem_dealloc(tbase, 512);
+  }
+}
+
+// Joins the slices of a row: out = sum_s 2^(ref_s - ref) O_s / sum_s 2^(ref_s - ref) l_s with
+// ref the largest.  One warp per row; D/32 columns per lane.
+template <int D>
+__global__ void __launch_bounds__(256) attend_dense_join_kernel(
+    const float* __restrict__ part, const float2* __restrict__ part_ml, int nq, int nsplit,
+    long long rows, void* __restrict__ out, int out_dtype, float* __restrict__ lse) {
+  constexpr int kPer = D / 32;
+  const long long r = static_cast<long long>(blockIdx.x) * 8 + threadIdx.x / 32;
+  const int lane = threadIdx.x % 32;
+  if (r >= rows) return;
+  const size_t base = static_cast<size_t>(r / nq) * nsplit * nq + static_cast<size_t>(r % nq);
+  float m = -INFINITY;
+  for (int s = lane; s < nsplit; s += 32) m = fmaxf(m, part_ml[base + static_cast<size_t>(s) * nq].x);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  float l = 0.f, acc[kPer] = {};
+  for (int s = 0; s < nsplit; ++s) {
+    const size_t at = base + static_cast<size_t>(s) * nq;
+    const float2 ml = part_ml[at];
+    if (ml.y == 0.f) continue;                             // a slice without a live key
+    const float w = ex2_approx(ml.x - m);
+    l = fmaf(w, ml.y, l);
+    const float* src = part + at * D + lane * kPer;
+    if constexpr (kPer == 4) {
+      const float4 v = *reinterpret_cast<const float4*>(src);
+      acc[0] = fmaf(w, v.x, acc[0]), acc[1] = fmaf(w, v.y, acc[1]);
+      acc[2] = fmaf(w, v.z, acc[2]), acc[3] = fmaf(w, v.w, acc[3]);
+    } else {
+      const float2 v = *reinterpret_cast<const float2*>(src);
+      acc[0] = fmaf(w, v.x, acc[0]), acc[1] = fmaf(w, v.y, acc[1]);
+    }
+  }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  const size_t at = static_cast<size_t>(r) * D + lane * kPer;
+#pragma unroll
+  for (int j = 0; j < kPer; j += 2) {
+    if (out_dtype == 1)
+      *reinterpret_cast<float2*>(static_cast<float*>(out) + at + j) =
+          make_float2(acc[j] * inv, acc[j + 1] * inv);
+    else
+      *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(out) + at + j) =
+          pack_bf16(acc[j] * inv, acc[j + 1] * inv);
+  }
+  if (lane == 0 && lse != nullptr) lse[r] = (m + log2f(l)) * kLn2;
+}
+
+// Slices of the key tiles per query tile (pair): the count with the least estimated time on 148
+// SMs, one CTA each.  A tile is taken as 1 unit (both query tiles of a pair: 2), a CTA's start
+// and end as 4, the join kernel as 5 plus the partial sums' traffic.
+int attend_dense_splits(int H, int nq, int nk, int nc, int d) {
+  constexpr int kSms = 148;
+  const long long qt = (static_cast<long long>(nq) + 127) / 128;
+  const long long units = static_cast<long long>(H) * (qt > 1 ? (qt + 1) / 2 : 1);
+  const long long T = (static_cast<long long>(nk) + 127) / 128 + (nc + 127) / 128;
+  int best = 1;
+  double least = 0;
+  for (int s = 1; s <= kMaxSplits && (s == 1 || 2 * s <= T); ++s) {
+    const long long waves = (units * s + kSms - 1) / kSms;
+    const double bytes = static_cast<double>(H) * nq * d * 8.0 * s;
+    if (s > 1 && bytes > 512e6) break;
+    const double cost = static_cast<double>(waves) *
+                            (static_cast<double>((T + s - 1) / s) * (qt > 1 ? 2 : 1) + 4) +
+                        (s > 1 ? 5 + bytes / 4e6 : 0);
+    if (s == 1 || cost < least) least = cost, best = s;
+  }
+  return best;
+}
+
+size_t attend_dense_workspace(int H, int nq, int nk, int nc, int d) {
+  const int s = attend_dense_splits(H, nq, nk, nc, d);
+  if (s == 1) return 256;
+  const size_t rows = static_cast<size_t>(H) * nq * s;
+  return (rows * d * 4 + 255) / 256 * 256 + (rows * 8 + 255) / 256 * 256;
+}
+
+template <int D, bool kPair>
+static cudaError_t launch_dense_t(const DenseMaps& m, int H, int nq, int nk, int nc,
+                                  const int32_t* ranges, int nsplit, void* out, int out_dtype,
+                                  float* lse, float* part, float2* ml, uint32_t* err,
+                                  cudaStream_t s) {
+  auto kern = attend_dense_kernel<D, kPair>;
+  constexpr size_t smem = Cfg<D, kPair>::kSmem;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       static_cast<int>(smem));
+  if (e != cudaSuccess) return e;
+  const dim3 grid(kPair ? (nq + 255) / 256 : 1, nsplit, H);
+  kern<<<grid, kThreads, smem, s>>>(m.q, m.k, m.v, m.kc, m.vc, nq, nk, nc,
+                                    reinterpret_cast<const int4*>(ranges), nsplit, out, out_dtype,
+                                    lse, part, ml, err, wait_limit_ns());
+  return cudaGetLastError();
+}
+
+cudaError_t launch_attend_dense(const DenseMaps& maps, int H, int nq, int nk, int nc, int d,
+                                const int32_t* ranges, void* out, int out_dtype, float* lse,
+                                void* workspace, uint32_t* err, cudaStream_t s) {
+  const int nsplit = attend_dense_splits(H, nq, nk, nc, d);
+  const long long rows = static_cast<long long>(H) * nq;
+  float* part = static_cast<float*>(workspace);
+  const size_t part_bytes = (static_cast<size_t>(rows) * nsplit * d * 4 + 255) / 256 * 256;
+  float2* ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + part_bytes);
+  cudaError_t e;
+  if (d == 128)
+    e = nq > 128 ? launch_dense_t<128, true>(maps, H, nq, nk, nc, ranges, nsplit, out, out_dtype,
+                                             lse, part, ml, err, s)
+                 : launch_dense_t<128, false>(maps, H, nq, nk, nc, ranges, nsplit, out, out_dtype,
+                                              lse, part, ml, err, s);
+  else
+    e = nq > 128 ? launch_dense_t<64, true>(maps, H, nq, nk, nc, ranges, nsplit, out, out_dtype,
+                                            lse, part, ml, err, s)
+                 : launch_dense_t<64, false>(maps, H, nq, nk, nc, ranges, nsplit, out, out_dtype,
+                                             lse, part, ml, err, s);
+  if (e != cudaSuccess || nsplit == 1) return e;
+  const unsigned grid = static_cast<unsigned>((rows + 7) / 8);
+  if (d == 128)
+    attend_dense_join_kernel<128><<<grid, 256, 0, s>>>(part, ml, nq, nsplit, rows, out, out_dtype,
+                                                       lse);
+  else
+    attend_dense_join_kernel<64><<<grid, 256, 0, s>>>(part, ml, nq, nsplit, rows, out, out_dtype,
+                                                      lse);
+  return cudaGetLastError();
+}
+
+// ------------------------------------------------------------------------------ key ranges
+
+// Row i of segment b (the one whose queries q_offsets[b] .. q_offsets[b+1]-1 hold i): the whole
+// of the segment's video keys and of its context keys, the latter ended at
+// max(prefix_b, i - first + 1 + context - queries) when causal.  Rows of no segment are empty.
+__global__ void __launch_bounds__(256) attend_ranges_kernel(
+    int nq, int nseg, const int32_t* __restrict__ q_offsets,
+    const int32_t* __restrict__ k_offsets, const int32_t* __restrict__ c_offsets,
+    const int32_t* __restrict__ prefix, int causal, int4* __restrict__ ranges, uint32_t* err) {
+  const int i = blockIdx.x * 256 + threadIdx.x;
+  if (i >= nq) return;
+  // the last b with q_offsets[b] <= i
+  int lo = 0, hi = nseg + 1;
+  while (lo < hi) {
+    const int mid = (lo + hi) / 2;
+    if (q_offsets[mid] <= i) lo = mid + 1; else hi = mid;
+  }
+  const int b = lo - 1;
+  int4 r = make_int4(0, 0, 0, 0);
+  if (b >= 0 && b < nseg) {
+    const int q0 = q_offsets[b], q1 = q_offsets[b + 1];
+    bool bad = false;
+    if (k_offsets != nullptr) {
+      r.x = k_offsets[b], r.y = k_offsets[b + 1];
+      bad |= r.x < 0 || r.y < r.x;
+    }
+    if (c_offsets != nullptr) {
+      const int c0 = c_offsets[b], c1 = c_offsets[b + 1];
+      bad |= c0 < 0 || c1 < c0;
+      r.z = c0, r.w = c1;
+      if (causal) {
+        long long end = static_cast<long long>(i) - q0 + 1 + (static_cast<long long>(c1) - c0) -
+                        (static_cast<long long>(q1) - q0);
+        if (prefix != nullptr) end = max(end, static_cast<long long>(prefix[b]));
+        end = min(max(end, 0ll), static_cast<long long>(c1) - c0);
+        r.w = static_cast<int>(c0 + end);
+      }
+    }
+    if (bad) {
+      r = make_int4(0, 0, 0, 0);
+      flag_error(err, kErrOffsets);
+    }
+  }
+  ranges[i] = r;
+}
+
+cudaError_t launch_attend_ranges(int nq, int nseg, const int32_t* q_offsets,
+                                 const int32_t* k_offsets, const int32_t* c_offsets,
+                                 const int32_t* prefix, int causal, int32_t* ranges,
+                                 uint32_t* err, cudaStream_t s) {
+  attend_ranges_kernel<<<(nq + 255) / 256, 256, 0, s>>>(nq, nseg, q_offsets, k_offsets, c_offsets,
+                                                        prefix, causal,
+                                                        reinterpret_cast<int4*>(ranges), err);
+  return cudaGetLastError();
+}
+
+}  // namespace spark

@@ -93,6 +93,41 @@ cudaError_t launch_quant_fp8(const void* src, int H, int R, int d, const int32_t
                              int ngroups, void* dst, float* scales, uint32_t* err,
                              cudaStream_t s);
 
+// ---- Dense attention over the video and the context keys (dense.cu)
+// TMA descriptors (encode_rows_map) of Q [H,nq,d], K, V [H,nk,d] and Kc, Vc [H,nc,d], all bf16;
+// those of an empty key set are never loaded through.
+struct DenseMaps {
+  CUtensorMap q, k, v, kc, vc;
+};
+// Slices the key tiles are cut into (1: no workspace is read), and the workspace's bytes.
+int attend_dense_splits(int H, int nq, int nk, int nc, int d);
+size_t attend_dense_workspace(int H, int nq, int nk, int nc, int d);
+// ranges: optional [nq,4] {video begin, end, context begin, end}; lse: optional [H,nq].
+cudaError_t launch_attend_dense(const DenseMaps& maps, int H, int nq, int nk, int nc, int d,
+                                const int32_t* ranges, void* out, int out_dtype, float* lse,
+                                void* workspace, uint32_t* err, cudaStream_t s);
+cudaError_t launch_attend_ranges(int nq, int nseg, const int32_t* q_offsets,
+                                 const int32_t* k_offsets, const int32_t* c_offsets,
+                                 const int32_t* prefix, int causal, int32_t* ranges,
+                                 uint32_t* err, cudaStream_t s);
+
+// ---- Per-head norm and rotation of queries and keys (rope.cu)
+constexpr int kMaxRopeAxes = 4;
+// Everything but the tensors: rotated pairs per head, the first pair of every position axis
+// (first[naxes] == pairs), strides in elements.
+struct RopeArgs {
+  const void* in[3];                 // Q, K, V (null: absent)
+  void* out[3];                      // [H,N,d] contiguous
+  long long head_stride[3], token_stride[3];
+  const float* weight[2];            // null: not normalised
+  const void* positions;             // [N,naxes] int32 or fp32
+  const float* inv_freq;             // [pairs]
+  float eps, scale;
+  int H, N, pairs, naxes, positions_f32, interleaved;
+  int first[kMaxRopeAxes + 1];
+};
+cudaError_t launch_qk_norm_rope(const RopeArgs& a, int dtype, int d, cudaStream_t s);
+
 // ---- Spark-Reblock partitioner (reblock.cu)
 // Byte offsets of its workspace regions (256-byte aligned).
 struct ReblockLayout {

@@ -233,8 +233,8 @@ SPARK_API spark_status spark_bsa_attend(const void* Qp, const void* Kp, const vo
  * as Q/K/V).  Every video query attends to all of them exactly, in the same row-wise softmax
  * as the exact and compressed branches (logit sigma q.kc_j).  They form no block and take no
  * part in the anchor, the block means, the summaries or the routing; k is still taken over the
- * nkb video blocks.  Context queries are not part of this operation (the caller attends them
- * densely).  0 <= nc <= SPARK_MAX_NC; nc == 0 is exactly the call without context. */
+ * nkb video blocks.  Context queries are not part of this operation (spark_attend_dense attends
+ * them, spark_bsa_forward_joint runs both).  0 <= nc <= SPARK_MAX_NC; nc == 0 is exactly the call without context. */
 
 /* Workspace bytes spark_bsa_forward_ctx needs: spark_bsa_workspace_size plus two bf16
  * [H,nc,d] regions (each rounded up to 256 bytes) that receive the converted context rows at
@@ -520,6 +520,124 @@ SPARK_API spark_status spark_bsa_forward_noalloc(const void* Q, const void* K, c
                                                  const int32_t* q_block_offsets, int nqb,
                                                  const int32_t* k_block_offsets, int nkb,
                                                  double topk_ratio, void* out, void* stream);
+
+/* ---- Per-head norm and rotation of queries and keys ----
+ * No counterpart in the pages (their Q, K, V arrive prepared): what a video transformer does to
+ * its projections' output before any call here, in one pass that also lays Q, K and V out as
+ * [H,N,d].  Row (h,n) of Q (and of K, with its own weights), x its d values:
+ *   y = x * rsqrt(mean(x^2) + eps) * w                       (w NULL: y = x)
+ *   pair i of the 2*pairs leading values: (y_i, y_{i+pairs}), or (y_{2i}, y_{2i+1}) when
+ *   `interleaved` is non-zero, becomes
+ *     rope_scale * (a cos t - b sin t, a sin t + b cos t),   t = pos[n,axis(i)] * inv_freq[i]
+ *   and the values behind the rotated ones pass unscaled.
+ * V's rows are copied.  fp32 arithmetic, angles reduced in fp64, one rounding to `dtype`.
+ *   - Q: required; K, V: NULL when absent.  d in {64,128}; dtype SPARK_BF16 or SPARK_F32.
+ *   - strides (HOST, NULL for contiguous [H,N,d]): six element strides, {head, token} of Q, of K
+ *     and of V; the d values of a row are contiguous.  Any alignment of whole elements works;
+ *     16-byte aligned rows and halves are read and written widest.
+ *   - q_weight, k_weight: device fp32 [d], NULL for no norm.  eps >= 0, finite.
+ *   - positions: device [N,naxes] int32, or fp32 when positions_f32 is non-zero; axis_pairs
+ *     (HOST, [naxes]) >= 0, summing to `pairs` <= d/2, gives the pairs that follow each axis, in
+ *     order; inv_freq: device fp32 [pairs].  1 <= naxes <= SPARK_MAX_ROPE_AXES.  With pairs == 0
+ *     nothing is rotated and positions, axis_pairs and inv_freq may be NULL.
+ *   - Q_out, K_out, V_out: device contiguous [H,N,d] of `dtype`.  An output may be its own input
+ *     when that is contiguous [H,N,d]; the tensors must not overlap otherwise. */
+#define SPARK_MAX_ROPE_AXES 4
+
+SPARK_API spark_status spark_qk_norm_rope(const void* Q, const void* K, const void* V, int dtype,
+                                          int H, int N, int d, const int64_t* strides,
+                                          const float* q_weight, const float* k_weight,
+                                          double eps, const void* positions, int positions_f32,
+                                          int naxes, const int32_t* axis_pairs, int pairs,
+                                          const float* inv_freq, int interleaved,
+                                          double rope_scale, void* Q_out, void* K_out,
+                                          void* V_out, void* stream);
+
+/* Rotation frequencies of the axes, one after the other, into inv_freq (HOST fp32, the sum of
+ * axis_pairs) and the factor for rope_scale into *rope_scale (HOST; 1 but for YaRN).  Pure host
+ * arithmetic in fp64.  Axis of n pairs (2n rotated values): f_i = base^(-i/n), i < n, and for a
+ * context `factor` (>= 1) times as long as the `original` positions of the training:
+ *   SPARK_ROPE_NONE    f_i
+ *   SPARK_ROPE_LINEAR  f_i / factor (position interpolation)
+ *   SPARK_ROPE_NTK     base grows by factor^(n/(n-1)): the slowest pair is stretched by factor,
+ *                      the fastest kept (n = 1: f_0)
+ *   SPARK_ROPE_YARN    f_i where the pair turns more than 32 times over `original` positions,
+ *                      f_i / factor where it turns less than once, a linear ramp over i between
+ *                      (Peng et al., YaRN, arXiv 2309.00071), and *rope_scale = 0.1 ln(factor) + 1.
+ * base > 1.  `original` is read by YaRN only (> 0 then). */
+#define SPARK_ROPE_NONE 0
+#define SPARK_ROPE_LINEAR 1
+#define SPARK_ROPE_NTK 2
+#define SPARK_ROPE_YARN 3
+
+SPARK_API spark_status spark_rope_frequencies(const int32_t* axis_pairs, int naxes, double base,
+                                              int scaling, double factor, double original,
+                                              float* inv_freq, double* rope_scale);
+
+/* ---- Dense attention over the video and the context keys ----
+ * Spark-H3 blog, section "Spark-Reblock": context/sink tokens stay exact, so their own queries
+ * attend everything; its benchmark keeps the first layer and the warm-up steps dense.  Row i of
+ * head h attends the video keys j in [r0,r1) and the context keys j in [r2,r3) of its ranges:
+ *   s_j = sigma Q[h,i] . key_j,  out[h,i] = sum_j exp(s_j - lse) value_j,  lse = log sum exp s_j
+ * (sigma = 1/sqrt(d)).  A row without a key has out = 0 and lse = -inf.
+ *   - Q: [H,nq,d], K, V: [H,nk,d], Kc, Vc: [H,nc,d], bf16, contiguous, 16-byte aligned; K and V
+ *     may be NULL when nk == 0, Kc and Vc when nc == 0.  One set of keys per query head.
+ *     nq >= 1; nk, nc >= 0; nq, nk <= SPARK_MAX_DENSE, nc <= SPARK_MAX_NC.  d in {64,128}.
+ *   - ranges: device int32 [nq,4], 16-byte aligned, shared by all heads: {r0, r1, r2, r3} per row,
+ *     cut to [0,nk) and [0,nc) (r1 <= r0: none of the video keys).  NULL: every row attends all.
+ *     spark_attend_ranges builds those of packed segments.
+ *   - out: [H,nq,d] of out_dtype; lse: fp32 [H,nq], may be NULL.  Neither may overlap an input.
+ *   - workspace: device, 256-byte aligned, spark_attend_dense_workspace_size bytes (never 0): the
+ *     partial sums of calls with few rows, whose keys are split over the GPU and joined by a
+ *     second kernel in a fixed order (results are deterministic).
+ *   - Keys of a row's masked places may hold anything, NaN included.  A value row may when no row
+ *     of the same 256 consecutive query rows (128 when nq <= 128) has it between the smallest
+ *     begin and the largest end of its ranges; elsewhere 0 * NaN reaches the rows that mask it.
+ *   - bf16 tensor-core products with fp32 sums; probabilities are rounded to bf16. */
+#define SPARK_MAX_DENSE (1 << 30)
+
+/* Workspace bytes of spark_attend_dense; 0 if the sizes are invalid. */
+SPARK_API size_t spark_attend_dense_workspace_size(int H, int nq, int nk, int nc, int d);
+
+SPARK_API spark_status spark_attend_dense(const void* Q, const void* K, const void* V,
+                                          const void* Kc, const void* Vc, int H, int nq, int nk,
+                                          int nc, int d, const int32_t* ranges, void* out,
+                                          int out_dtype, float* lse, void* workspace,
+                                          size_t workspace_bytes, uint32_t* err, void* stream);
+
+/* Key ranges of nq query rows of nseg packed segments (documents, clips with their prompts),
+ * built on the device from segment offsets, so that lengths need not reach the host:
+ *   - segment b holds the query rows q_offsets[b] .. q_offsets[b+1]-1, the video keys
+ *     k_offsets[b] .. k_offsets[b+1]-1 and the context keys c_offsets[b] .. c_offsets[b+1]-1
+ *     (device int32 [nseg+1] each, non-decreasing; k_offsets and c_offsets may be NULL: none);
+ *   - a row's ranges are the keys of its segment; with `causal` non-zero its context range ends
+ *     behind max(prefix[b], l + 1 + context length - query length) keys of the segment (l the
+ *     row's place in it, so the last query sees all; prefix: device int32 [nseg], NULL for 0);
+ *   - rows of no segment (padding behind the last) get the empty ranges {0,0,0,0}.
+ * ranges: device int32 [nq,4], 16-byte aligned.  A segment whose key offsets are negative or
+ * decrease sets SPARK_DEVERR_OFFSETS in err (may be NULL) and its rows are empty. */
+SPARK_API spark_status spark_attend_ranges(int nq, int nseg, const int32_t* q_offsets,
+                                           const int32_t* k_offsets, const int32_t* c_offsets,
+                                           const int32_t* prefix, int causal, int32_t* ranges,
+                                           uint32_t* err, void* stream);
+
+/* The attention of a block whose context tokens are queries too: spark_bsa_forward_ctx for the
+ * video queries, then spark_attend_dense for the context queries Qc [H,nc,d] over every video
+ * and context key, with their output in out_c [H,nc,d] (both of `dtype`).  nc >= 1.  The keys of
+ * the dense part are the workspace's reblocked ones (their order does not matter).  workspace:
+ * spark_bsa_workspace_size_joint bytes, starting with spark_bsa_forward_ctx's. */
+SPARK_API size_t spark_bsa_workspace_size_joint(int H, int N, int d, int nqb, int nkb,
+                                                double topk_ratio, int nc);
+
+SPARK_API spark_status spark_bsa_forward_joint(const void* Q, const void* K, const void* V,
+                                               const void* Qc, const void* Kc, const void* Vc,
+                                               int nc, int dtype, int H, int N, int d,
+                                               const int32_t* q_perm, const int32_t* k_perm,
+                                               const int32_t* q_block_offsets, int nqb,
+                                               const int32_t* k_block_offsets, int nkb,
+                                               double topk_ratio, void* out, void* out_c,
+                                               void* workspace, size_t workspace_bytes,
+                                               void* stream);
 
 #ifdef __cplusplus
 }

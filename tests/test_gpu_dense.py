@@ -1,0 +1,387 @@
+"""GPU tests of the dense attention over video and context keys and of the key ranges, against
+the definition in 64 bits.
+
+Tolerances, per output value, before any run: a probability is rounded to bf16 for the tensor
+cores (at most half a step, 2^-8 of it) while the sum that divides it is not, so the weighted sum
+is off by at most 2^-8 * A with A = sum_j p_j |v_j|; a bf16 output adds 2^-8 |out|.  The fp32 part:
+a score is a sum of 128 products, each addition off by at most 2^-23 (truncated) of at most
+sum |q k| sigma < 2^5 here, so 2^-11 at the very worst; it is held to 2^-12 of A, and the
+log-sum-exp to 2^-12.
+"""
+
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import _parity as P
+from block_sparse_attention_gather_b200 import (
+    DEVERR, spark_attend_dense, spark_attend_dense_workspace_size, spark_attend_ranges,
+    spark_bsa_forward_ctx, spark_bsa_forward_joint, spark_bsa_get_wait_limit_ns,
+    spark_bsa_read_error, spark_bsa_set_wait_limit_ns, spark_qk_norm_rope, spark_reblock,
+    spark_rope_frequencies, workspace_views)
+from test_gpu_parity import custom_inputs
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+BF = torch.bfloat16
+
+
+def inputs(seed, H, nq, nk, nc, d, scale=1.0):
+    g = torch.Generator(device=DEV).manual_seed(seed)
+
+    def rand(n, s=1.0):
+        return (torch.randn(H, n, d, generator=g, device=DEV) * s).to(BF)
+
+    return dict(Q=rand(nq, scale), K=rand(nk), V=rand(nk), Kc=rand(nc) if nc else None,
+                Vc=rand(nc) if nc else None)
+
+
+def reference(x, ranges=None, heads=None):
+    """(out, lse, sum p |v|) of the given heads in 64 bits."""
+    H, nq, d = x["Q"].shape
+    nk = x["K"].shape[1]
+    outs = []
+    for h in range(H) if heads is None else heads:
+        k, v = x["K"][h].double(), x["V"][h].double()
+        if x["Kc"] is not None:
+            k, v = torch.cat([k, x["Kc"][h].double()]), torch.cat([v, x["Vc"][h].double()])
+        s = x["Q"][h].double() @ k.T / math.sqrt(d)
+        if ranges is not None:
+            j = torch.arange(k.shape[0], device=DEV)
+            r = ranges.long()[:, :, None]
+            live = ((j >= r[:, 0]) & (j < r[:, 1]) & (j < nk)) | \
+                ((j - nk >= r[:, 2].clamp(min=0)) & (j - nk < r[:, 3]))
+            s = torch.where(live, s, torch.full_like(s, -math.inf))
+        lse = torch.logsumexp(s, dim=1)
+        p = torch.exp(s - torch.where(lse.isinf(), torch.zeros_like(lse), lse)[:, None])
+        # a masked value takes no part, whatever it holds
+        v = torch.where(torch.isfinite(v), v, torch.zeros_like(v))
+        outs.append((p @ v, lse, p @ v.abs()))
+    return [torch.stack(t) for t in zip(*outs)]
+
+
+def check(x, out, lse, ranges=None, heads=None):
+    ref, rl, A = reference(x, ranges, heads)
+    if heads is not None:
+        out, lse = out[list(heads)], lse[list(heads)]
+    got = out.double()
+    assert torch.isfinite(got).all()
+    tol = (2.0 ** -8 + 2.0 ** -12) * A + (2.0 ** -8 * ref.abs() if out.dtype == BF else 0) + 1e-30
+    worst = ((got - ref).abs() / tol).max().item()
+    assert worst <= 1.0, f"output off by {worst:.2f} of its tolerance"
+    empty = torch.isinf(rl)
+    assert torch.equal(torch.isinf(lse), empty) and (lse[empty] < 0).all()
+    assert (got[empty] == 0).all()
+    if (~empty).any():
+        assert (lse.double() - rl)[~empty].abs().max().item() <= 2.0 ** -12
+
+
+SIZES = [(1, 1, 1, 0, 128), (2, 1, 129, 0, 64), (3, 127, 300, 5, 128), (2, 128, 0, 77, 64),
+         (1, 129, 1000, 1, 128), (2, 257, 511, 130, 64), (1, 300, 40000, 300, 128),
+         (24, 1, 5000, 0, 128), (2, 513, 128, 128, 64), (2, 700, 2000, 0, 128),
+         (5, 3, 20001, 77, 64)]
+
+
+@pytest.mark.parametrize("H,nq,nk,nc,d", SIZES)
+@pytest.mark.parametrize("dtype", [BF, torch.float32])
+def test_all_keys(H, nq, nk, nc, d, dtype):
+    x = inputs(11 + nq, H, nq, nk, nc, d)
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    out, lse = spark_attend_dense(**x, out_dtype=dtype, err=err)
+    assert spark_bsa_read_error(err) == 0
+    check(x, out, lse)
+
+
+def random_ranges(seed, nq, nk, nc):
+    """Ranges of every kind: whole, short, one key, empty, reversed, past both ends."""
+    rng = np.random.default_rng(seed)
+    r = np.zeros((nq, 4), dtype=np.int64)
+    for i in range(nq):
+        for at, n in ((0, nk), (2, nc)):
+            a, b = sorted(rng.integers(0, n + 1, 2))
+            kind = rng.integers(0, 6)
+            if kind == 0:
+                a, b = 0, n
+            elif kind == 1:
+                b = min(a + 1, n)
+            elif kind == 2:
+                b = a
+            elif kind == 3:
+                a, b = b, a
+            elif kind == 4:
+                a, b = -5, n + 1000
+            r[i, at], r[i, at + 1] = a, b
+    return torch.from_numpy(r.astype(np.int32)).to(DEV)
+
+
+@pytest.mark.parametrize("H,nq,nk,nc,d", SIZES)
+def test_any_ranges(H, nq, nk, nc, d):
+    x = inputs(23 + nq, H, nq, nk, nc, d)
+    r = random_ranges(nq, nq, nk, nc)
+    out, lse = spark_attend_dense(**x, ranges=r, out_dtype=torch.float32)
+    check(x, out, lse, r)
+
+
+@pytest.mark.parametrize("nq", [1, 100, 300])
+def test_every_row_empty(nq):
+    x = inputs(5, 2, nq, 700, 30, 128)
+    r = torch.tensor([[9, 9, 30, 30]], dtype=torch.int32, device=DEV).repeat(nq, 1)
+    out, lse = spark_attend_dense(**x, ranges=r)
+    assert (out == 0).all() and (lse == -math.inf).all()
+
+
+@pytest.mark.parametrize("nq", [1, 200])
+def test_no_keys_at_all(nq):
+    x = inputs(6, 2, nq, 0, 0, 64)
+    out, lse = spark_attend_dense(**x)
+    assert (out == 0).all() and (lse == -math.inf).all()
+
+
+@pytest.mark.parametrize("nq", [3, 128, 300])
+@pytest.mark.parametrize("step", [0.05, 3.0])
+def test_maximum_that_keeps_growing(nq, step):
+    """Scores that rise along the keys: the running reference has to follow."""
+    H, nk, d = 2, 1500, 128
+    x = inputs(7, H, nq, nk, 40, d)
+    u = torch.ones(d, device=DEV) / math.sqrt(d)
+    x["Q"] = (x["Q"].float() * 0.1 + 4 * u).to(BF)
+    ramp = torch.linspace(0, step * 12, nk, device=DEV)[None, :, None]
+    x["K"] = (x["K"].float() * 0.1 + ramp * u * math.sqrt(d)).to(BF)
+    out, lse = spark_attend_dense(**x, out_dtype=torch.float32)
+    ref, rl, A = reference(x)
+    # scores reach 144: their fp32 sums are off by up to 2^-23 * 128 * 144 < 2^-8 at the worst
+    assert ((out.double() - ref).abs() <= (2.0 ** -8 + 2.0 ** -7) * A).all()
+    assert (lse.double() - rl).abs().max() <= 2.0 ** -8
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("nq", [1, 130, 256])
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
+def test_masked_places_may_hold_anything(nq, d, bad):
+    x = inputs(8, 2, nq, 700, 200, d)
+    lo, hi, clo, chi = 130, 601, 3, 77
+    for k in ("K", "V"):
+        x[k][:, :lo] = bad
+        x[k][:, hi:] = bad
+        x[k + "c"][:, :clo] = bad
+        x[k + "c"][:, chi:] = bad
+    r = torch.tensor([[lo, hi, clo, chi]], dtype=torch.int32, device=DEV).repeat(nq, 1)
+    if nq > 2:
+        r[1] = torch.tensor([5, 5, 9, 2])                  # a row of nothing
+        r[2] = torch.tensor([lo + 7, lo + 8, 0, 0])        # a row of one key
+    out, lse = spark_attend_dense(**x, ranges=r, out_dtype=torch.float32)
+    for k in ("K", "V"):
+        x[k][:, :lo] = 0
+        x[k][:, hi:] = 0
+        x[k + "c"][:, :clo] = 0
+        x[k + "c"][:, chi:] = 0
+    check(x, out, lse, r)
+
+
+def test_nan_in_a_live_key_reaches_its_rows_only():
+    x = inputs(9, 1, 2, 600, 0, 128)
+    x["K"][0, 500] = math.nan
+    r = torch.tensor([[0, 600, 0, 0], [0, 400, 0, 0]], dtype=torch.int32, device=DEV)
+    out, lse = spark_attend_dense(**x, ranges=r)
+    assert torch.isnan(out[0, 0]).all() and torch.isnan(lse[0, 0])
+    x["K"][0, 500] = 0
+    ref, rl, A = reference(x, r)
+    assert ((out[0, 1].double() - ref[0, 1]).abs() <= 2.0 ** -7 * A[0, 1] + 1e-6).all()
+
+
+def test_keys_past_32_bit_offsets():
+    """4.6 GB of keys: byte and element offsets beyond 2^32 and 2^31."""
+    H, nk, d = 3, 6_000_000, 128
+    g = torch.Generator(device=DEV).manual_seed(3)
+    K = torch.zeros(H, nk, d, dtype=BF, device=DEV)
+    V = torch.zeros(H, nk, d, dtype=BF, device=DEV)
+    n = 1000
+    K[:, -n:] = torch.randn(H, n, d, generator=g, device=DEV).to(BF)
+    V[:, -n:] = torch.randn(H, n, d, generator=g, device=DEV).to(BF)
+    Q = torch.randn(H, 2, d, generator=g, device=DEV).to(BF)
+    r = torch.tensor([[nk - n, nk, 0, 0], [nk - 1, nk, 0, 0]], dtype=torch.int32, device=DEV)
+    out, lse = spark_attend_dense(Q, K, V, ranges=r, out_dtype=torch.float32)
+    x = dict(Q=Q, K=K[:, -n:].contiguous(), V=V[:, -n:].contiguous(), Kc=None, Vc=None)
+    r2 = torch.tensor([[0, n, 0, 0], [n - 1, n, 0, 0]], dtype=torch.int32, device=DEV)
+    check(x, out, lse, r2)
+
+
+def test_results_are_deterministic_and_workspace_independent():
+    x = inputs(10, 4, 77, 9000, 77, 128)
+    size = spark_attend_dense_workspace_size(4, 77, 9000, 77, 128)
+    a = spark_attend_dense(**x)
+    ws = torch.full((size + 1024,), 255, dtype=torch.uint8, device=DEV)
+    b = spark_attend_dense(**x, workspace=ws)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+@pytest.mark.parametrize("nq", [1, 300])
+def test_on_another_stream_and_in_graphs_that_share_a_workspace(nq):
+    x = inputs(12, 2, nq, 9000, 33, 128)
+    y = inputs(13, 2, nq, 9000, 33, 128)
+    want = [spark_attend_dense(**t) for t in (x, y)]
+    size = spark_attend_dense_workspace_size(2, nq, 9000, 33, 128)
+    ws = torch.empty(size, dtype=torch.uint8, device=DEV)
+    outs = [(torch.empty_like(w[0]), torch.empty_like(w[1])) for w in want]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    spark_attend_dense(**x, out=outs[0][0], lse=outs[0][1], workspace=ws, stream=side)
+    side.synchronize()
+    assert torch.equal(outs[0][0], want[0][0])
+    graphs = []
+    for t, (o, l) in zip((x, y), outs):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            spark_attend_dense(**t, out=o, lse=l, workspace=ws)
+        graphs.append(graph)
+    for o, l in outs:
+        o.zero_(), l.zero_()
+    for _ in range(3):
+        for graph in graphs:
+            graph.replay()
+    torch.cuda.synchronize()
+    for (o, l), w in zip(outs, want):
+        assert torch.equal(o, w[0]) and torch.equal(l, w[1])
+
+
+@pytest.mark.parametrize("nq", [5, 300])
+def test_expired_wait_is_flagged_and_leaves_the_context_usable(nq):
+    x = inputs(14, 2, nq, 3000, 10, 128)
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    old = spark_bsa_get_wait_limit_ns()
+    try:
+        spark_bsa_set_wait_limit_ns(0)
+        spark_attend_dense(**x, err=err)
+        torch.cuda.synchronize()
+    finally:
+        spark_bsa_set_wait_limit_ns(old)
+    assert err.item() == DEVERR["timeout"]
+    err.zero_()
+    out, lse = spark_attend_dense(**x, err=err)
+    assert spark_bsa_read_error(err) == 0
+    check(x, out, lse)
+
+
+# ------------------------------------------------------------------------------ key ranges
+
+def ranges_reference(nq, q, k, c, prefix, causal):
+    out = np.zeros((nq, 4), dtype=np.int32)
+    for b in range(len(q) - 1):
+        for i in range(q[b], min(q[b + 1], nq)):
+            if k is not None:
+                out[i, :2] = k[b], k[b + 1]
+            if c is not None:
+                lc, end = c[b + 1] - c[b], c[b + 1] - c[b]
+                if causal:
+                    seen = i - q[b] + 1 + lc - (q[b + 1] - q[b])
+                    end = min(max(seen, prefix[b] if prefix is not None else 0, 0), lc)
+                out[i, 2:] = c[b], c[b] + end
+    return out
+
+
+@pytest.mark.parametrize("nseg,rows,pad", [(1, 1, 0), (1, 50, 3), (7, 300, 0), (64, 40, 9),
+                                           (1000, 5000, 100)])
+@pytest.mark.parametrize("causal", [False, True])
+def test_ranges_of_segments(nseg, rows, pad, causal):
+    rng = np.random.default_rng(nseg + rows)
+
+    def offsets(total):
+        return np.concatenate([[0], np.sort(rng.integers(0, total + 1, nseg - 1)), [total]])
+
+    q, k, c = offsets(rows), offsets(70000), offsets(rows + 20)
+    prefix = rng.integers(-3, 40, nseg)
+    dev = [torch.tensor(t, dtype=torch.int32, device=DEV) for t in (q, k, c, prefix)]
+    for use in ((1, 1, 1), (1, 0, 0), (0, 1, 0), (0, 0, 0)):
+        kk, cc = (dev[1] if use[0] else None), (dev[2] if use[1] else None)
+        pp = dev[3] if use[2] and causal else None
+        got = spark_attend_ranges(rows + pad, dev[0], kk, cc, prefix=pp, causal=causal)
+        want = ranges_reference(rows + pad, q, k if use[0] else None, c if use[1] else None,
+                                prefix if pp is not None else None, causal)
+        assert np.array_equal(got.cpu().numpy(), want)
+
+
+def test_ranges_refuse_decreasing_key_offsets_in_the_error_word():
+    q = torch.tensor([0, 2, 4], dtype=torch.int32, device=DEV)
+    k = torch.tensor([0, 9, 5], dtype=torch.int32, device=DEV)
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    got = spark_attend_ranges(4, q, k, err=err)
+    assert err.item() == DEVERR["offsets"]
+    assert got.tolist() == [[0, 9, 0, 0]] * 2 + [[0, 0, 0, 0]] * 2
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("causal", [False, True])
+def test_packed_prompts_equal_one_call_per_clip(d, causal):
+    """Segments of every length, zero and one among them, and rows of padding at the end."""
+    ql, kl = [77, 0, 1, 200, 130], [500, 64, 1, 0, 1303]
+    q = torch.tensor(np.cumsum([0] + ql), dtype=torch.int32, device=DEV)
+    k = torch.tensor(np.cumsum([0] + kl), dtype=torch.int32, device=DEV)
+    nq = sum(ql) + 7
+    x = inputs(15, 2, nq, sum(kl), nq, d)
+    for t in ("Kc", "Vc"):
+        x[t][:, sum(ql):] = math.nan                       # padding of the prompts
+    r = spark_attend_ranges(nq, q, k, q, causal=causal)
+    out, lse = spark_attend_dense(**x, ranges=r, out_dtype=torch.float32)
+    for t in ("Kc", "Vc"):
+        x[t][:, sum(ql):] = 0
+    check(x, out, lse, r)
+    assert (out[:, sum(ql):] == 0).all()
+
+
+# ------------------------------------------------------------- together, as they are used
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("nc", [1, 77, 300])
+def test_joint_forward(dtype, nc):
+    x = custom_inputs(31, 2, 1500, 128, dtype, 30, 128)
+    H, N, d = x["Q"].shape
+    g = torch.Generator().manual_seed(4)
+    for n in ("Qc", "Kc", "Vc"):
+        x[n] = torch.randn(H, nc, d, generator=g).to(x["Q"].dtype).to(DEV)
+    perms = (x["q_perm"], x["k_perm"], x["q_offsets"], x["k_offsets"])
+    out, out_c, ws, layout = spark_bsa_forward_joint(x["Q"], x["K"], x["V"], x["Qc"], x["Kc"],
+                                                     x["Vc"], *perms, 0.2)
+    views = workspace_views(ws, layout, H, N, d, x["q_offsets"].numel() - 1,
+                            x["k_offsets"].numel() - 1)
+    assert spark_bsa_read_error(views["err"]) == 0
+    want, _, _ = spark_bsa_forward_ctx(x["Q"], x["K"], x["V"], x["Kc"], x["Vc"], *perms, 0.2)
+    assert torch.equal(out, want)
+    # the context queries against the definition, on the bf16 values the kernels see
+    b = {n: x[n].to(BF) for n in ("K", "V", "Kc", "Vc")}
+    b["Q"] = x["Qc"].to(BF)
+    ref, _, A = reference(b)
+    tol = (2.0 ** -8 + 2.0 ** -12) * A + (2.0 ** -8 * ref.abs() if dtype == "bf16" else 0)
+    assert out_c.dtype == x["Q"].dtype
+    assert ((out_c.double() - ref).abs() <= tol).all()
+
+
+def test_projection_to_joint_attention():
+    """A fused projection's output through norm and rotation, the partitioner and the joint
+    attention, against the same steps in 64 bits where they are not the sparse call itself."""
+    H, N, nc, d = 2, 1280, 77, 128
+    g = torch.Generator(device=DEV).manual_seed(21)
+    video = torch.randn(N, 3, H, d, generator=g, device=DEV).to(BF)
+    text = torch.randn(nc, 3, H, d, generator=g, device=DEV).to(BF)
+    w = [(1 + 0.1 * torch.randn(d, generator=g, device=DEV)) for _ in range(2)]
+    axes = [16, 24, 24]
+    freq, scale = spark_rope_frequencies(axes)
+    pos = torch.stack(torch.meshgrid(*(torch.arange(n) for n in (5, 16, 16)), indexing="ij"),
+                      dim=-1).reshape(-1, 3).int().to(DEV)
+    Q, K, V = (video[:, i].transpose(0, 1) for i in range(3))
+    Q, K, V = spark_qk_norm_rope(Q, K, V, *w, positions=pos, inv_freq=freq.to(DEV),
+                                 axis_pairs=axes, interleaved=True, rope_scale=scale)
+    Qc, Kc, Vc = (text[:, i].transpose(0, 1) for i in range(3))
+    Qc, Kc, Vc = spark_qk_norm_rope(Qc, Kc, Vc, *w)
+    q_perm, k_perm, offsets = spark_reblock(Q, K, block=128)
+    out, out_c, ws, layout = spark_bsa_forward_joint(Q, K, V, Qc, Kc, Vc, q_perm, k_perm, offsets,
+                                                     offsets, 1.0)
+    views = workspace_views(ws, layout, H, N, d, offsets.numel() - 1, offsets.numel() - 1)
+    assert spark_bsa_read_error(views["err"]) == 0
+    # ratio 1: every block is exact, so the video rows are dense attention too
+    dense, lse = spark_attend_dense(Q, K, V, Kc, Vc, out_dtype=torch.float32)
+    check(dict(Q=Q, K=K, V=V, Kc=Kc, Vc=Vc), dense, lse)
+    P.compare_out(P.to64(out), P.to64(dense), "video rows at ratio 1")
+    ref, _, A = reference(dict(Q=Qc, K=K, V=V, Kc=Kc, Vc=Vc))
+    assert ((out_c.double() - ref).abs() <= (2.0 ** -8 + 2.0 ** -12) * A + 2.0 ** -8 * ref.abs()).all()
