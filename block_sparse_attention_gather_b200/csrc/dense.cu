@@ -8,17 +8,18 @@
 //
 // One pass over the keys with a running reference per row (an online softmax):
 //   p_j = 2^(s_j log2e - ref),  l = sum p,  O = sum p v,  out = O / l,  lse = (ref + log2 l) ln2.
-// ref starts as the row's maximum over its first tile with a live key and follows the running
-// maximum only when that exceeds ref by more than 2^8 (then O and l are rescaled): between
-// rescales p stays under 2^8 and its rounding to bf16 for the tensor cores is relative, so a
-// reference below the true maximum costs no accuracy.  l and O are fp32.
+// ref is the row's maximum over its first tile with a live key.  It is raised to a later tile's
+// maximum, and O and l rescaled, only when that tile's sum of p reaches 2^24 (or is no number):
+// up to there p, rounded to bf16 for the tensor cores, and the fp32 sums keep their relative
+// accuracy, so a reference below the true maximum costs none, and the usual tile needs no
+// maximum at all.  The scores stay in TMEM until the sum is known, so the tile can be redone.
 //
 // One CTA works on one head, one slice of the key tiles, and
 //   kPair:  two 128-row query tiles, one per softmax group; every K and V tile serves both;
 //   !kPair: one 128-row query tile; the groups take the even and the odd key tiles, each with
 //           its own O, and the epilogue joins them.
-// 10 warps: 0-3 / 4-7 the softmax groups (warp w owns TMEM lanes 32*(w%4)..), 8 the TMA
-// producer, 9 the MMA issuer.  TMEM columns: S_g at 128 g (P_g written over it as bf16), O_g at
+// 12 warps: 0-3 / 4-7 the softmax groups (warp w owns TMEM lanes 32*(w%4)..), 8 the TMA
+// producer, 9 the MMA issuer, 10 the watch of the loaded tiles.  TMEM columns: S_g at 128 g (P_g written over it as bf16), O_g at
 // 256 + D g.  The next S of a group is issued behind the PV that reads its P, so the commit that
 // announces S(t+1) also tells that PV(t) is complete and O may be rescaled.
 //
@@ -29,6 +30,7 @@
 // Every wait is bounded (see spark_ptx.cuh); on expiry the kernel flags kErrTimeout, drains its
 // copies and MMAs, frees TMEM and returns.
 #include <climits>
+#include <type_traits>
 
 #include "spark_kernels.cuh"
 
@@ -36,12 +38,17 @@ namespace spark {
 
 namespace {
 
-constexpr int kWarpLoad = 8, kWarpMma = 9;
-constexpr int kThreads = 320;
+constexpr int kWarpLoad = 8, kWarpMma = 9, kWarpTiles = 10;
+constexpr int kThreads = 384;                // three warpgroups; warp 11 only gives registers
+// Registers a thread: 168 at launch (all the SM has for 384 threads), then moved from the third
+// warpgroup to the softmax ones; 2 * kRegsSoftmax + kRegsOther == 3 * kRegsLaunch.
+constexpr int kRegsLaunch = 168, kRegsSoftmax = 208, kRegsOther = 88;
+static_assert(2 * kRegsSoftmax + kRegsOther == 3 * kRegsLaunch, "register split");
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kLag = 8.f;                  // log2 units the reference may lag the maximum by
+constexpr float kMaxSum = 0x1p24f;           // a tile's sum of p from which the reference is raised
 constexpr int kMaxSplits = 64;
+constexpr int kPolyEvery = 4;                // one pair of exponentials in 4 by the polynomial
 
 template <int D, bool kPair>
 struct Cfg {
@@ -73,12 +80,66 @@ struct Tiles {
   }
 };
 
+// Warp-wide bounded wait (all lanes): true once the phase of `bar` with parity `parity` is
+// complete, false after an abort, as mbar_wait.  The lanes test together, so the warp stays
+// converged, and only a few tests apart from the abort checks, which read global memory.
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
+                                          uint32_t* err, uint64_t limit_ns) {
+  constexpr uint32_t kAll = 0xffffffffu;
+  if (limit_ns != 0 && __all_sync(kAll, mbar_test(bar, parity))) return true;
+  const uint64_t t0 = globaltimer_ns();
+  for (;;) {
+    bool ok = true;
+    if (limit_ns == 0 || globaltimer_ns() - t0 >= limit_ns) {
+      flag_error(err, kErrTimeout);
+      *abort_flag = 1;
+      ok = false;
+    } else if (*abort_flag) {
+      ok = false;
+    } else if (launch_timed_out(err)) {
+      *abort_flag = 1;
+      ok = false;
+    }
+    if (!__all_sync(kAll, ok)) return false;
+    for (int i = 0; i < 8; ++i)
+      if (__all_sync(kAll, mbar_test_sleep(bar, parity, 20000u))) return true;
+  }
+}
+
 __device__ __forceinline__ bool drain(uint64_t* bar, uint32_t parity) {
   const uint64_t t0 = globaltimer_ns();
   while (!mbar_test(bar, parity)) {
     if (globaltimer_ns() - t0 > kWaitLimitNs) return false;
   }
   return true;
+}
+
+// NaN if either is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+// 2^a of two values without the special-function unit: 2^a = 2^n 2^f, n the nearest integer
+// (taken by adding 1.5 * 2^23, which leaves n in the low bits), 2^f on [-1/2, 1/2] by a degree-4
+// polynomial fitted for the least largest relative error (2.7e-6 in fp32; the result is rounded
+// to bf16, 2^-9).  Arguments under -126 give 2^-126 and NaN gives a number: the caller's other
+// values of the row carry a NaN.
+__device__ __forceinline__ void ex2_poly2(uint64_t a2, float& p0, float& p1) {
+  float a0, a1;
+  f2_unpack(a2, a0, a1);
+  a2 = f2_pack(fmaxf(a0, -126.f), fmaxf(a1, -126.f));
+  const uint64_t r2 = f2_add(a2, f2_splat(12582912.f));
+  const uint64_t f2 = f2_fma(f2_add(r2, f2_splat(-12582912.f)), f2_splat(-1.f), a2);
+  uint64_t y = f2_fma(f2_splat(0.009570101906375769f), f2, f2_splat(0.05591786031900944f));
+  y = f2_fma(y, f2, f2_splat(0.2402474482798183f));
+  y = f2_fma(y, f2, f2_splat(0.6931218147367589f));
+  y = f2_fma(y, f2, f2_splat(0.9999992614456781f));
+  float y0, y1, r0, r1;
+  f2_unpack(y, y0, y1);
+  f2_unpack(r2, r0, r1);
+  p0 = __int_as_float(__float_as_int(y0) + (__float_as_int(r0) << 23));
+  p1 = __int_as_float(__float_as_int(y1) + (__float_as_int(r1) << 23));
 }
 
 // Order of the tiles in the shared-memory ring: the order in which the MMA warp first uses them.
@@ -92,18 +153,109 @@ __device__ __forceinline__ int slot_v(int t, int T) {
   return kPair ? 2 * t + 1 : min(2 * t + 2, 2 * T - 1);
 }
 
-__device__ __forceinline__ float max128(const float (&x)[128]) {
-  float mx[4] = {x[0], x[1], x[2], x[3]};
+// 32 columns of this thread's TMEM row without waiting; tmem_wait32 completes it (the registers
+// pass through the wait, so that no use moves before it).
+__device__ __forceinline__ void tmem_ld32_issue(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : SPARK_R8(0), SPARK_R8(8), SPARK_R8(16), SPARK_R8(24)
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : SPARK_R8(0), SPARK_R8(8)
+      : "r"(taddr)
+      : "memory");
+}
+#define SPARK_RW8(b) "+r"(r[b + 0]), "+r"(r[b + 1]), "+r"(r[b + 2]), "+r"(r[b + 3]), \
+                     "+r"(r[b + 4]), "+r"(r[b + 5]), "+r"(r[b + 6]), "+r"(r[b + 7])
+__device__ __forceinline__ void tmem_wait32(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : SPARK_RW8(0), SPARK_RW8(8), SPARK_RW8(16), SPARK_RW8(24)
+               :
+               : "memory");
+}
+
+// Bits lo .. hi-1 of 32 (either bound may lie outside).
+__device__ __forceinline__ uint32_t bits32(int lo, int hi) {
+  auto below = [](int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; };
+  return below(hi) & ~below(lo);
+}
+
+// p of 32 scores (raw; those whose bit of `live` is clear masked when kExact) as packed bf16
+// pairs; returns their sum (two partial ones).  kExact: every exponential by the special-function
+// unit, so that a masked place is an exact zero; otherwise one pair in kPolyEvery by the
+// polynomial.
+template <bool kExact>
+__device__ __forceinline__ uint64_t exp32(const uint32_t (&r)[32], uint32_t live, uint64_t c2,
+                                          uint64_t nm2, uint32_t (&pk)[16]) {
+  uint64_t sum2[2] = {0, 0};
 #pragma unroll
-  for (int j = 4; j < 124; j += 8) {
-    mx[0] = fmax3(mx[0], x[j], x[j + 1]);
-    mx[1] = fmax3(mx[1], x[j + 2], x[j + 3]);
-    mx[2] = fmax3(mx[2], x[j + 4], x[j + 5]);
-    mx[3] = fmax3(mx[3], x[j + 6], x[j + 7]);
+  for (int j = 0; j < 16; ++j) {
+    float x0 = __uint_as_float(r[2 * j]), x1 = __uint_as_float(r[2 * j + 1]);
+    if (kExact) {
+      if (!(live & (1u << (2 * j)))) x0 = -INFINITY;
+      if (!(live & (2u << (2 * j)))) x1 = -INFINITY;
+    }
+    const uint64_t a2 = f2_fma(f2_pack(x0, x1), c2, nm2);
+    float p0, p1;
+    if (!kExact && j % kPolyEvery == kPolyEvery - 1) {
+      ex2_poly2(a2, p0, p1);
+    } else {
+      float a0, a1;
+      f2_unpack(a2, a0, a1);
+      p0 = ex2_approx(a0), p1 = ex2_approx(a1);
+    }
+    sum2[j & 1] = f2_add(sum2[j & 1], f2_pack(p0, p1));
+    pk[j] = pack_bf16(p0, p1);
   }
-  mx[0] = fmax3(mx[0], x[124], x[125]);
-  mx[1] = fmax3(mx[1], x[126], x[127]);
-  return fmaxf(fmax3(mx[0], mx[1], mx[2]), mx[3]);
+  return f2_add(sum2[0], sum2[1]);
+}
+
+// The tile's 128 scores at `sbuf` -> packed pairs, returning the sum of p; columns outside
+// [lo, hi) are masked when kExact.  The load of the next 32 columns is in flight while the
+// current ones are exponentiated.
+template <bool kExact>
+__device__ __forceinline__ float exp_tile(uint32_t sbuf, int lo, int hi, float c, float m,
+                                          uint32_t (&pk)[4][16]) {
+  const uint64_t c2 = f2_splat(c), nm2 = f2_splat(-m);
+  uint32_t ra[32], rb[32];
+  tmem_ld32_issue(sbuf, ra);
+  tmem_wait32(ra);
+  tmem_ld32_issue(sbuf + 32, rb);
+  uint64_t s = exp32<kExact>(ra, kExact ? bits32(lo, hi) : 0u, c2, nm2, pk[0]);
+  tmem_wait32(rb);
+  tmem_ld32_issue(sbuf + 64, ra);
+  s = f2_add(s, exp32<kExact>(rb, kExact ? bits32(lo - 32, hi - 32) : 0u, c2, nm2, pk[1]));
+  tmem_wait32(ra);
+  tmem_ld32_issue(sbuf + 96, rb);
+  s = f2_add(s, exp32<kExact>(ra, kExact ? bits32(lo - 64, hi - 64) : 0u, c2, nm2, pk[2]));
+  tmem_wait32(rb);
+  s = f2_add(s, exp32<kExact>(rb, kExact ? bits32(lo - 96, hi - 96) : 0u, c2, nm2, pk[3]));
+  float s0, s1;
+  f2_unpack(s, s0, s1);
+  return s0 + s1;
+}
+
+// Maximum of the tile's scores (raw) of columns [lo, hi), NaN if one is; -inf if there is none.
+__device__ __forceinline__ float max_tile(uint32_t sbuf, int lo, int hi) {
+  float mx = -INFINITY;
+#pragma unroll 1
+  for (int cc = 0; cc < 128; cc += 32) {
+    uint32_t r[32];
+    tmem_ld32(sbuf + cc, r);
+    const uint32_t live = bits32(lo - cc, hi - cc);
+#pragma unroll
+    for (int j = 0; j < 32; ++j)
+      if (live & (1u << j)) mx = max_nan(mx, __uint_as_float(r[j]));
+  }
+  return mx;
 }
 
 }  // namespace
@@ -119,6 +271,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_dense_kernel(
   using C = Cfg<D, kPair>;
   constexpr int kStages = C::kStages;
   constexpr int kAtoms = D / 64;
+  constexpr int kAhead = kPair ? 1 : 2;                   // tiles from one of a group to its next
   constexpr uint32_t kAll = 0xffffffffu;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
@@ -136,7 +289,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_dense_kernel(
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   const int h = blockIdx.z, split = blockIdx.y;
   const int q0 = blockIdx.x * (kPair ? 256 : 128);
-  const int groups = kPair && q0 + 128 < nq ? 2 : 1;      // query tiles with rows (kPair)
+  const int groups = !kPair || q0 + 128 < nq ? 2 : 1;     // a pair's second query tile may be void
 
   // This thread's row and its key ranges; rows past nq count as unmasked and are never stored.
   const int grp = (warp >> 2) & 1, q4 = warp & 3;
@@ -148,8 +301,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_dense_kernel(
     int4 r = make_int4(INT_MAX, 0, INT_MAX, 0);
     if (live) {
       if (ranges != nullptr) rg = ranges[qi];
-      rg.x = max(rg.x, 0), rg.y = min(rg.y, nk);
-      rg.z = max(rg.z, 0), rg.w = min(rg.w, nc);
+      rg.x = max(rg.x, 0), rg.y = max(min(rg.y, nk), 0);
+      rg.z = max(rg.z, 0), rg.w = max(min(rg.w, nc), 0);
       if (rg.x < rg.y) r.x = rg.x, r.y = rg.y;
       if (rg.z < rg.w) r.z = rg.z, r.w = rg.w;
     }
@@ -167,7 +320,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_dense_kernel(
     }
     for (int g = 0; g < 2; ++g) {
       mbar_init(&bars.sfull[g], 1);
-      mbar_init(&bars.pready[g], 128);
+      mbar_init(&bars.pready[g], 128 + 1);                // the group's rows and the tiles
     }
     mbar_init(&bars.done, 1);
     mbar_fence_init();
@@ -198,6 +351,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_dense_kernel(
   }
   const int T = tl.count;
 
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
   if (warp == kWarpLoad) {
     // -------------------------------------------------------------------- TMA producer
     int issued = 0;
@@ -205,8 +360,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_dense_kernel(
       if (elect_one()) {
         tma_prefetch_desc(&map_k);
         tma_prefetch_desc(&map_v);
-        mbar_arrive_expect_tx(&bars.qfull, groups * C::kTile);
-        for (int g = 0; g < groups; ++g)
+        const int qtiles = kPair ? groups : 1;
+        mbar_arrive_expect_tx(&bars.qfull, qtiles * C::kTile);
+        for (int g = 0; g < qtiles; ++g)
           for (int a = 0; a < kAtoms; ++a)
             tma_load_3d(qst + g * C::kTile + a * 16384, &map_q, &bars.qfull, a * 64,
                         q0 + g * 128, h);
@@ -218,8 +374,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_dense_kernel(
         const int t = is_k ? nk_done++ : nv_done++;
         const int s = i % kStages;
         if (i >= kStages &&
-            !__all_sync(kAll, mbar_wait(&bars.empty[s], ((i / kStages) - 1) & 1, abort_flag, err,
-                                        wait_ns)))
+            !wait_warp(&bars.empty[s], ((i / kStages) - 1) & 1, abort_flag, err, wait_ns))
           break;
         if (elect_one()) {
           mbar_arrive_expect_tx(&bars.full[s], C::kTile);
@@ -238,162 +393,150 @@ __global__ void __launch_bounds__(kThreads, 1) attend_dense_kernel(
     }
   } else if (warp == kWarpMma) {
     // ---------------------------------------------------------------------- MMA issuer
+    // Per tile and group one wait, for P and what the tile warp has seen land, then O += P V and
+    // the group's next S over that P back to back.
     constexpr uint32_t idS = idesc_bf16(128, 128, false, false);
     constexpr uint32_t idO = idesc_bf16(128, D, false, true);
     const uint64_t qd = sdesc_sw128(smem_u32(qst), 16, 1024);
     const uint64_t kd0 = sdesc_sw128(smem_u32(ring), 16, 1024);
     const uint64_t vd0 = sdesc_sw128(smem_u32(ring), 16384, 1024);
-    bool ok = T > 0 && __all_sync(kAll, mbar_wait(&bars.qfull, 0, abort_flag, err, wait_ns));
-    auto wait_full = [&](int i) {
-      return __all_sync(kAll, mbar_wait(&bars.full[i % kStages], (i / kStages) & 1, abort_flag,
-                                        err, wait_ns));
-    };
-    // S of key tile t into group g's buffer; the last reader of the K tile frees its stage
-    auto issue_s = [&](int t, int g, bool last) -> bool {
+    // one lane: the group's S of key tile t; the tile's last reader frees its stage
+    auto mma_s = [&](int t, int g) {
       const int i = slot_k<kPair>(t);
-      if (!wait_full(i)) return false;
       const uint64_t kd = kd0 + static_cast<uint64_t>((i % kStages) * (C::kTile >> 4));
       const uint64_t q = qd + static_cast<uint64_t>(kPair ? g * (C::kTile >> 4) : 0);
-      if (elect_one()) {
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t off = ((kk / 4) * 16384 + (kk % 4) * 32) / 16;
-          mma_ss(tbase + g * 128, q + off, kd + off, idS, kk > 0 ? 1u : 0u);
-        }
-        tc_commit(&bars.sfull[g]);
-        if (last) tc_commit(&bars.empty[i % kStages]);
+      for (int kk = 0; kk < D / 16; ++kk) {
+        const uint32_t off = ((kk / 4) * 16384 + (kk % 4) * 32) / 16;
+        mma_ss(tbase + g * 128, q + off, kd + off, idS, kk > 0 ? 1u : 0u);
       }
-      __syncwarp();
-      return true;
+      tc_commit(&bars.sfull[g]);
+      if (!kPair || g + 1 == groups) tc_commit(&bars.empty[i % kStages]);
     };
-    // O_g += P V of key tile t (the n-th tile of the group)
-    auto issue_pv = [&](int t, int g, int n, bool last) -> bool {
-      if (!__all_sync(kAll, mbar_wait(&bars.pready[g], n & 1, abort_flag, err, wait_ns)))
-        return false;
-      tc_fence_after_sync();
+    // one lane: O_g += P V of key tile t, `first` the group's first
+    auto mma_pv = [&](int t, int g, bool first) {
       const int i = slot_v<kPair>(t, T);
-      if (!wait_full(i)) return false;
       const uint64_t vd = vd0 + static_cast<uint64_t>((i % kStages) * (C::kTile >> 4));
-      if (elect_one()) {
 #pragma unroll
-        for (int kk = 0; kk < 8; ++kk)
-          mma_ts(tbase + 256 + g * D, tbase + g * 128 + kk * 8, vd + (kk * 2048) / 16, idO,
-                 (kk > 0 || n > 0) ? 1u : 0u);
-        if (last) tc_commit(&bars.empty[i % kStages]);
-      }
-      __syncwarp();
-      return true;
+      for (int kk = 0; kk < 8; ++kk)
+        mma_ts(tbase + 256 + g * D, tbase + g * 128 + kk * 8, vd + (kk * 2048) / 16, idO,
+               (kk > 0 || !first) ? 1u : 0u);
+      if (!kPair || g + 1 == groups) tc_commit(&bars.empty[i % kStages]);
     };
-    if constexpr (kPair) {
-      for (int g = 0; ok && g < groups; ++g) ok = issue_s(0, g, g + 1 == groups);
-      for (int t = 0; ok && t < T; ++t)
-        for (int g = 0; ok && g < groups; ++g) {
-          ok = issue_pv(t, g, t, g + 1 == groups);
-          if (ok && t + 1 < T) ok = issue_s(t + 1, g, g + 1 == groups);
+    auto wait_full = [&](int i) {
+      return wait_warp(&bars.full[i % kStages], (i / kStages) & 1, abort_flag, err, wait_ns);
+    };
+    bool ok = T > 0 && wait_warp(&bars.qfull, 0, abort_flag, err, wait_ns);
+    for (int t = 0; ok && t < (kPair ? 1 : min(T, 2)); ++t) {
+      if (!(ok = wait_full(slot_k<kPair>(t)))) break;
+      if (elect_one())
+        for (int g = kPair ? 0 : t; g < (kPair ? groups : t + 1); ++g) mma_s(t, g);
+      __syncwarp();
+    }
+    for (int t = 0; ok && t < T; ++t) {
+      const bool more = t + kAhead < T;
+      for (int g = kPair ? 0 : t & 1; g < (kPair ? groups : (t & 1) + 1); ++g) {
+        ok = wait_warp(&bars.pready[g], (kPair ? t : t >> 1) & 1, abort_flag, err, wait_ns);
+        if (!ok) break;
+        tc_fence_after_sync();
+        if (elect_one()) {
+          mma_pv(t, g, kPair ? t == 0 : t < 2);
+          if (more) mma_s(t + kAhead, g);
         }
-    } else {
-      for (int t = 0; ok && t < min(T, 2); ++t) ok = issue_s(t, t, true);
-      for (int t = 0; ok && t < T; ++t) {
-        ok = issue_pv(t, t & 1, t >> 1, true);
-        if (ok && t + 2 < T) ok = issue_s(t + 2, t & 1, true);
+        __syncwarp();
       }
     }
     // every MMA complete: the epilogue reads O, and TMEM is freed after
     if (elect_one()) tc_commit(&bars.done);
     __syncwarp();
     drain(&bars.done, 0);
+  } else if (warp == kWarpTiles) {
+    // ---------------------------------------------------------------------- tile watch
+    // Waits for the V tile and the group's next K tile in the MMA warp's stead and arrives at
+    // pready for them: a barrier test takes a few hundred cycles while the MMAs read shared
+    // memory, and the MMA warp's are all in the way.
+    for (int t = 0; t < T; ++t) {
+      const int i = slot_v<kPair>(t, T), j = slot_k<kPair>(t + kAhead);
+      bool ok = wait_warp(&bars.full[i % kStages], (i / kStages) & 1, abort_flag, err, wait_ns);
+      if (ok && t + kAhead < T)
+        ok = wait_warp(&bars.full[j % kStages], (j / kStages) & 1, abort_flag, err, wait_ns);
+      for (int g = kPair ? 0 : t & 1; ok && g < (kPair ? groups : (t & 1) + 1); ++g) {
+        const int n = kPair ? t : t >> 1;
+        // the phase before has to be over, or this would count for it
+        if (n > 0) ok = wait_warp(&bars.pready[g], (n - 1) & 1, abort_flag, err, wait_ns);
+        if (ok && elect_one()) mbar_arrive(&bars.pready[g]);
+        __syncwarp();
+      }
+      if (!ok) break;
+    }
+  }
   } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
     // -------------------------------------------------------------------- softmax rows
     const uint32_t lane_off = static_cast<uint32_t>(q4 * 32) << 16;
-    const uint32_t sbuf = tbase + lane_off + grp * 128;
     const uint32_t obuf = tbase + lane_off + 256 + grp * D;
     const float c = kLog2e * rsqrtf(static_cast<float>(D));
     const bool warp_live = __any_sync(kAll, live);         // else nothing of this warp is stored
     float ref = -INFINITY, l = 0.f;                        // log2 units; sum of 2^(. - ref)
+    const uint32_t sbuf = tbase + lane_off + grp * 128;
     const int ntiles = kPair ? (grp < groups ? T : 0) : (T + 1 - grp) / 2;
     bool ok = true;
     for (int n = 0; n < ntiles; ++n) {
       const int t = kPair ? n : 2 * n + grp;
-      ok = __all_sync(kAll, mbar_wait(&bars.sfull[grp], n & 1, abort_flag, err, wait_ns));
+      ok = wait_warp(&bars.sfull[grp], n & 1, abort_flag, err, wait_ns);
       if (!ok) break;
       tc_fence_after_sync();
       const int y = tl.row(t);
       const bool video = tl.video(t);
       if (warp_live) {
-        float x[128];
-        {
-          uint32_t r[64];
-          tmem_ld64(sbuf, r);
-#pragma unroll
-          for (int j = 0; j < 64; ++j) x[j] = __uint_as_float(r[j]);
-          tmem_ld64(sbuf + 64, r);
-#pragma unroll
-          for (int j = 0; j < 64; ++j) x[64 + j] = __uint_as_float(r[j]);
+        const int lo = (video ? rg.x : rg.z) - y, hi = (video ? rg.y : rg.w) - y;
+        const bool edge = __any_sync(kAll, lo > 0 || hi < 128);
+        uint32_t pk[4][16];
+        float sum = 0.f;
+        // a row without a reference that sees its first keys needs the maximum at once
+        bool rise = __any_sync(kAll, ref == -INFINITY && max(lo, 0) < min(hi, 128));
+        if (!rise) {
+          const float m = ref == -INFINITY ? 0.f : ref;    // no live key yet: every p is 0
+          sum = edge ? exp_tile<true>(sbuf, lo, hi, c, m, pk)
+                     : exp_tile<false>(sbuf, lo, hi, c, m, pk);
+          rise = __any_sync(kAll, !(sum < kMaxSum));
         }
-        const int lo = max((video ? rg.x : rg.z) - y, 0);
-        const int hi = min((video ? rg.y : rg.w) - y, 128);
-        if (__any_sync(kAll, lo > 0 || hi < 128)) {
-          const unsigned width = static_cast<unsigned>(max(hi - lo, 0));
-#pragma unroll
-          for (int j = 0; j < 128; ++j)
-            if (static_cast<unsigned>(j - lo) >= width) x[j] = -INFINITY;
-        }
-        const float mx = max128(x) * c;
-        const bool grow = mx > ref + kLag;
-        if (__any_sync(kAll, grow)) {
-          const float next = grow ? mx : ref;
+        if (rise) {
+          const float mx = max_tile(sbuf, lo, hi) * c;
+          const bool grow = !(mx <= ref);                  // a NaN among the scores too
+          // a score of +inf leaves no number to compare the others with
+          const float next = grow ? (mx < INFINITY ? mx : NAN) : ref;
           const float f = grow ? ex2_approx(ref - next) : 1.f;
           ref = next;
           l *= f;
           if (n > 0) {
+#pragma unroll 1
+            for (int cc = 0; cc < D; cc += 16) {
+              uint32_t o[16];
+              tmem_ld16(obuf + cc, o);
 #pragma unroll
-            for (int cc = 0; cc < D; cc += 32) {
-              uint32_t o[32];
-              tmem_ld32(obuf + cc, o);
-              uint32_t o2[16];
-#pragma unroll
-              for (int hh = 0; hh < 2; ++hh) {
-#pragma unroll
-                for (int j = 0; j < 16; ++j)
-                  o2[j] = __float_as_uint(__uint_as_float(o[hh * 16 + j]) * f);
-                tmem_st16_issue(obuf + cc + hh * 16, o2);
-              }
+              for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+              tmem_st16_issue(obuf + cc, o);
             }
           }
+          sum = exp_tile<true>(sbuf, lo, hi, c, ref == -INFINITY ? 0.f : ref, pk);
         }
-        const float m = ref > -INFINITY ? ref : 0.f;       // no live key yet: every p is 0
-        const uint64_t c2 = f2_splat(c), nm2 = f2_splat(-m);
-        uint64_t sum2[2] = {0, 0};
+        l += sum;
 #pragma unroll
-        for (int cc = 0; cc < 128; cc += 32) {
-          uint32_t pk[16];
-#pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            const uint64_t a2 = f2_fma(f2_pack(x[cc + 2 * j], x[cc + 2 * j + 1]), c2, nm2);
-            float a0, a1;
-            f2_unpack(a2, a0, a1);
-            const float p0 = ex2_approx(a0), p1 = ex2_approx(a1);
-            sum2[j & 1] = f2_add(sum2[j & 1], f2_pack(p0, p1));
-            pk[j] = pack_bf16(p0, p1);
-          }
-          tmem_st16_issue(sbuf + cc / 2, pk);
-        }
-        float s0, s1;
-        f2_unpack(f2_add(sum2[0], sum2[1]), s0, s1);
-        l += s0 + s1;
+        for (int i = 0; i < 4; ++i) tmem_st16_issue(sbuf + 16 * i, pk[i]);
         tmem_wait_st();
       }
       // V rows past the hull that are not past the tensor (those TMA fills with zeros): zeroed
       // by group 0, whose P the MMA warp waits for first (kPair), or by the tile's own group
-      const int end = video ? tl.ve : tl.ce, rows = video ? nk : nc;
-      if (y + 128 > end && end < rows && (!kPair || grp == 0)) {
+      const int end = (video ? tl.ve : tl.ce) - y, rows = (video ? nk : nc) - y;
+      const bool zero = end < 128 && end < rows && (!kPair || grp == 0);
+      if (zero) {
         const int i = slot_v<kPair>(t, T);
-        ok = __all_sync(kAll, mbar_wait(&bars.full[i % kStages], (i / kStages) & 1, abort_flag,
-                                        err, wait_ns));
+        ok = wait_warp(&bars.full[i % kStages], (i / kStages) & 1, abort_flag, err, wait_ns);
         if (!ok) break;
         uint8_t* v = ring + (i % kStages) * C::kTile;
         for (int a = 0; a < kAtoms; ++a)
-          for (int k = (end - y) * 8 + row; k < 128 * 8; k += 128)
+          for (int k = end * 8 + row; k < 128 * 8; k += 128)
             *reinterpret_cast<uint4*>(v + a * 16384 + k * 16) = make_uint4(0, 0, 0, 0);
         fence_proxy_async_smem();
       }
@@ -402,7 +545,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_dense_kernel(
     }
     // ---- epilogue
     if (ok && T > 0)
-      ok = __all_sync(kAll, mbar_wait(&bars.done, 0, abort_flag, err, wait_ns));
+      ok = wait_warp(&bars.done, 0, abort_flag, err, wait_ns);
     float w[2] = {1.f, 1.f};                               // weights of the two groups' O
     bool read0 = true, read1 = false;                      // which hold something
     if constexpr (!kPair) {
@@ -414,11 +557,11 @@ __global__ void __launch_bounds__(kThreads, 1) attend_dense_kernel(
       w[0] = m0 > -INFINITY ? ex2_approx(m0 - ref) : 0.f;
       w[1] = m1 > -INFINITY ? ex2_approx(m1 - ref) : 0.f;
       l = w[0] * ex_l[0][row] + w[1] * ex_l[1][row];
-      read0 = T > 0, read1 = T > 1;
+      read0 = read1 = T > 0;
     } else {
       read0 = T > 0;
     }
-    if (ok && warp_live && (kPair ? grp < groups : true)) {
+    if (ok && warp_live && grp < groups) {
       tc_fence_after_sync();
       const size_t at = static_cast<size_t>(h) * nq + qi;
       const size_t prow = (static_cast<size_t>(h) * nsplit + split) * nq + qi;
@@ -568,6 +711,11 @@ static cudaError_t launch_dense_t(const DenseMaps& m, int H, int nq, int nk, int
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        static_cast<int>(smem));
   if (e != cudaSuccess) return e;
+  // the register split waits for registers that a launch with fewer would not have
+  cudaFuncAttributes attr;
+  e = cudaFuncGetAttributes(&attr, kern);
+  if (e != cudaSuccess) return e;
+  if (attr.numRegs != kRegsLaunch) return cudaErrorInvalidKernelImage;
   const dim3 grid(kPair ? (nq + 255) / 256 : 1, nsplit, H);
   kern<<<grid, kThreads, smem, s>>>(m.q, m.k, m.v, m.kc, m.vc, nq, nk, nc,
                                     reinterpret_cast<const int4*>(ranges), nsplit, out, out_dtype,

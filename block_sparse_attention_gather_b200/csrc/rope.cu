@@ -34,26 +34,28 @@ __device__ __forceinline__ void from_f(__nv_bfloat16& y, float x) { y = __float2
 }  // namespace
 
 // V: values per access (the two halves of V pairs are V values each); C: such accesses per
-// thread and half.
-template <typename T, int D, int V, int C>
+// thread and half; U: heads whose rows a thread holds at once.
+template <typename T, int D, int V, int C, int U>
 __global__ void __launch_bounds__(kRopeThreads) qk_norm_rope_kernel(const RopeArgs a,
                                                                     int heads_per_cta) {
   constexpr int kLanes = D / 2 / (V * C);          // threads per row
   constexpr int kTokens = kRopeThreads / kLanes;   // tokens per CTA
   using Vt = Vec<T, V>;
+  const int t = blockIdx.z == 0 ? 0 : (a.in[1] != nullptr ? blockIdx.z : 2);   // Q, K or V
   const int lane = threadIdx.x % kLanes;
   const long long n = static_cast<long long>(blockIdx.x) * kTokens + threadIdx.x / kLanes;
   const bool live = n < a.N;
   const int h0 = blockIdx.y * heads_per_cta, h1 = min(h0 + heads_per_cta, a.H);
+  const float* weight = t < 2 ? a.weight[t] : nullptr;
 
   // columns of the thread's two vectors, cos and sin of their pairs, norm weights
   int ca[C], cb[C];
   bool rot[C];
-  float cs[C][V], sn[C][V], w[2][C][2][V];
+  float cs[C][V], sn[C][V], w[C][2][V];
 #pragma unroll
   for (int c = 0; c < C; ++c) {
     const int p = (c * kLanes + lane) * V;         // first pair
-    rot[c] = p < a.pairs;
+    rot[c] = t < 2 && p < a.pairs;
     const bool half = rot[c] && !a.interleaved;
     ca[c] = half ? p : 2 * p;
     cb[c] = half ? p + a.pairs : 2 * p + V;
@@ -73,33 +75,30 @@ __global__ void __launch_bounds__(kRopeThreads) qk_norm_rope_kernel(const RopeAr
         sincospif(2.f * static_cast<float>(turns), &s, &k);
         cs[c][j] = k * a.scale, sn[c][j] = s * a.scale;
       }
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        w[t][c][0][j] = a.weight[t] != nullptr ? a.weight[t][ca[c] + j] : 1.f;
-        w[t][c][1][j] = a.weight[t] != nullptr ? a.weight[t][cb[c] + j] : 1.f;
-      }
+      w[c][0][j] = weight != nullptr ? weight[ca[c] + j] : 1.f;
+      w[c][1][j] = weight != nullptr ? weight[cb[c] + j] : 1.f;
     }
   }
-  const long long row0 = n * D;
-  for (int h = h0; h < h1; ++h) {
-    Vt x[3][C][2];
+  const T* src = static_cast<const T*>(a.in[t]) + n * a.token_stride[t];
+  T* dst = static_cast<T*>(a.out[t]) + n * D;
+  const long long hs = a.head_stride[t], hd = static_cast<long long>(a.N) * D;
+  for (int h = h0; h < h1; h += U) {
+    Vt x[U][C][2];
 #pragma unroll
-    for (int t = 0; t < 3; ++t) {
-      if (a.in[t] == nullptr || !live) continue;
-      const T* src = static_cast<const T*>(a.in[t]) + h * a.head_stride[t] + n * a.token_stride[t];
+    for (int u = 0; u < U; ++u) {
+      if (h + u >= h1 || !live) continue;
 #pragma unroll
       for (int c = 0; c < C; ++c) {
-        x[t][c][0] = *reinterpret_cast<const Vt*>(src + ca[c]);
-        x[t][c][1] = *reinterpret_cast<const Vt*>(src + cb[c]);
+        x[u][c][0] = *reinterpret_cast<const Vt*>(src + (h + u) * hs + ca[c]);
+        x[u][c][1] = *reinterpret_cast<const Vt*>(src + (h + u) * hs + cb[c]);
       }
     }
 #pragma unroll
-    for (int t = 0; t < 3; ++t) {
-      if (a.in[t] == nullptr) continue;
-      T* dst = static_cast<T*>(a.out[t]) + static_cast<long long>(h) * a.N * D + row0;
+    for (int u = 0; u < U; ++u) {
+      if (h + u >= h1) break;                      // uniform
       if (t < 2) {
         float r = 1.f;
-        if (a.weight[t] != nullptr) {
+        if (weight != nullptr) {
           float ss = 0.f;
           if (live) {
 #pragma unroll
@@ -108,7 +107,7 @@ __global__ void __launch_bounds__(kRopeThreads) qk_norm_rope_kernel(const RopeAr
               for (int e = 0; e < 2; ++e)
 #pragma unroll
                 for (int j = 0; j < V; ++j) {
-                  const float v = to_f(x[t][c][e].v[j]);
+                  const float v = to_f(x[u][c][e].v[j]);
                   ss = fmaf(v, v, ss);
                 }
           }
@@ -116,58 +115,64 @@ __global__ void __launch_bounds__(kRopeThreads) qk_norm_rope_kernel(const RopeAr
           for (int o = kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
           r = rsqrtf(ss * (1.f / D) + a.eps);
         }
-        if (!live) continue;
 #pragma unroll
         for (int c = 0; c < C; ++c) {
           float y[2 * V];
 #pragma unroll
           for (int e = 0; e < 2; ++e)
 #pragma unroll
-            for (int j = 0; j < V; ++j)
-              y[e * V + j] = to_f(x[t][c][e].v[j]) * r * w[t][c][e][j];
+            for (int j = 0; j < V; ++j) y[e * V + j] = to_f(x[u][c][e].v[j]) * r * w[c][e][j];
           if (rot[c]) {
             if (a.interleaved) {
 #pragma unroll
               for (int j = 0; j < V; ++j) {
-                const float u = y[2 * j], v = y[2 * j + 1];
-                y[2 * j] = u * cs[c][j] - v * sn[c][j];
-                y[2 * j + 1] = u * sn[c][j] + v * cs[c][j];
+                const float p = y[2 * j], q = y[2 * j + 1];
+                y[2 * j] = p * cs[c][j] - q * sn[c][j];
+                y[2 * j + 1] = p * sn[c][j] + q * cs[c][j];
               }
             } else {
 #pragma unroll
               for (int j = 0; j < V; ++j) {
-                const float u = y[j], v = y[V + j];
-                y[j] = u * cs[c][j] - v * sn[c][j];
-                y[V + j] = u * sn[c][j] + v * cs[c][j];
+                const float p = y[j], q = y[V + j];
+                y[j] = p * cs[c][j] - q * sn[c][j];
+                y[V + j] = p * sn[c][j] + q * cs[c][j];
               }
             }
           }
 #pragma unroll
           for (int e = 0; e < 2; ++e)
 #pragma unroll
-            for (int j = 0; j < V; ++j) from_f(x[t][c][e].v[j], y[e * V + j]);
+            for (int j = 0; j < V; ++j) from_f(x[u][c][e].v[j], y[e * V + j]);
         }
       }
-      if (!live) continue;
+      if (live) {
 #pragma unroll
-      for (int c = 0; c < C; ++c) {
-        *reinterpret_cast<Vt*>(dst + ca[c]) = x[t][c][0];
-        *reinterpret_cast<Vt*>(dst + cb[c]) = x[t][c][1];
+        for (int c = 0; c < C; ++c) {
+          *reinterpret_cast<Vt*>(dst + (h + u) * hd + ca[c]) = x[u][c][0];
+          *reinterpret_cast<Vt*>(dst + (h + u) * hd + cb[c]) = x[u][c][1];
+        }
       }
     }
   }
 }
 
+#ifndef RU
+#define RU 4
+#endif
+#ifndef RW
+#define RW 8
+#endif
 template <typename T, int D, int V, int C>
 static cudaError_t launch_rope_t(const RopeArgs& a, cudaStream_t s) {
   constexpr int kTokens = kRopeThreads / (D / 2 / (V * C));
   const int blocks = (a.N + kTokens - 1) / kTokens;
-  // few tokens: the heads go to more CTAs, until there are four per SM
-  int splits = (4 * 148 + blocks - 1) / blocks;
+  const int tensors = 1 + (a.in[1] != nullptr) + (a.in[2] != nullptr);
+  // few tokens: the heads go to more CTAs, until there are RW per SM
+  int splits = (RW * 148 + blocks * tensors - 1) / (blocks * tensors);
   if (splits > a.H) splits = a.H;
   const int per = (a.H + splits - 1) / splits;
-  qk_norm_rope_kernel<T, D, V, C>
-      <<<dim3(blocks, (a.H + per - 1) / per), kRopeThreads, 0, s>>>(a, per);
+  qk_norm_rope_kernel<T, D, V, C, RU>
+      <<<dim3(blocks, (a.H + per - 1) / per, tensors), kRopeThreads, 0, s>>>(a, per);
   return cudaGetLastError();
 }
 
