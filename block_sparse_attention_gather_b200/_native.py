@@ -877,16 +877,26 @@ def spark_bsa_forward_host(Q, K, V, q_perm, k_perm, q_offsets, k_offsets, topk_r
 
 # ------------------------------------------------ norm and rotation, dense attention
 
-def _on(dev):
-    """Makes `dev` current for a launch on one of its streams (a no-op when it is)."""
-    if dev.index == torch.cuda.current_device():
+def _on(index):
+    """Makes device `index` current for a launch on one of its streams (a no-op when it is)."""
+    if index == torch.cuda.current_device():
         return contextlib.nullcontext()
-    return torch.cuda.device(dev)
+    return torch.cuda.device(index)
 
 
-def _stream_of(dev, stream):
-    s = torch.cuda.current_stream(dev) if stream is None else stream
-    return ctypes.c_void_p(s.cuda_stream)
+def _stream_of(index, stream):
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(index)
+    return stream.cuda_stream
+
+
+def _check_one(t, name, dtype, device, index):
+    """_need for one dtype, the usual case in one expression: these calls can take as long on the
+    host as their kernels do on the GPU.  Returns the address."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == index
+            and t.is_contiguous()):
+        _need(t, name, dtype, device)
+    return t.data_ptr()
 
 
 def spark_rope_frequencies(axis_pairs, base=10000.0, scaling="none", factor=1.0, original=0.0):
@@ -903,20 +913,21 @@ def spark_rope_frequencies(axis_pairs, base=10000.0, scaling="none", factor=1.0,
     return out[:sum(int(p) for p in axis_pairs)], scale.value
 
 
-def _need_rows(t, name, dtype, shape, device):
-    """Like _need for a tensor whose last dimension alone has to be contiguous."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dtype not in (dtype if isinstance(dtype, tuple) else (dtype,)):
-        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
-    if t.dim() != 3 or (shape is not None and t.shape != shape):
+def _check_rows(t, name, dtype, shape, device, index):
+    """_check_one for a tensor [H, N, d] whose last dimension alone has to be contiguous."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == index
+            and t.dim() == 3):
+        _need(t.contiguous() if isinstance(t, torch.Tensor) else t, name, dtype, device)
+        raise ValueError(f"{name} must have the shape [H, N, d]")
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must have the shape [H, N, d] of Q")
-    if t.stride(2) != 1:
+    head, token, inner = t.stride()
+    if inner != 1:
         raise ValueError(f"{name}: the last dimension must be contiguous")
+    return t.data_ptr(), head, token
+
+
+_Strides = ctypes.c_int64 * 6
 
 
 def spark_qk_norm_rope(Q, K=None, V=None, q_weight=None, k_weight=None, eps=1e-6, positions=None,
@@ -927,53 +938,62 @@ def spark_qk_norm_rope(Q, K=None, V=None, q_weight=None, k_weight=None, eps=1e-6
     out along.  Weights fp32 [d] (None: no norm); positions [N, axes] int32 or fp32; inv_freq
     fp32 [pairs], axis_pairs the pairs of each axis (None: one axis).  Returns (Q_out, K_out,
     V_out), None for what is absent."""
-    _need_rows(Q, "Q", (torch.bfloat16, torch.float32), None, None)
-    dev, dt = Q.device, Q.dtype
-    H, N, d = Q.shape
-    ins, outs, strides = (Q, K, V), [Q_out, K_out, V_out], []
-    for i, name in enumerate("QKV"):
-        if ins[i] is None:
-            if outs[i] is not None:
-                raise ValueError(f"{name}_out given without {name}")
-            strides += [0, 0]
+    if not (isinstance(Q, torch.Tensor) and Q.is_cuda):
+        _need(Q, "Q")
+    dev, dt, shape = Q.device, Q.dtype, Q.shape
+    code, index = _code(dt), dev.index
+    q, qh, qt = _check_rows(Q, "Q", dt, None, dev, index)
+    H, N, d = shape
+    k = v = kh = kt = vh = vt = 0
+    if K is not None:
+        k, kh, kt = _check_rows(K, "K", dt, shape, dev, index)
+    elif K_out is not None or k_weight is not None:
+        raise ValueError("K_out and k_weight need K")
+    if V is not None:
+        v, vh, vt = _check_rows(V, "V", dt, shape, dev, index)
+    elif V_out is not None:
+        raise ValueError("V_out needs V")
+    outs = [Q_out, K_out, V_out]
+    ptrs = [None, None, None]
+    for i, x in enumerate((q, k, v)):
+        if x == 0 and i:
             continue
-        if i:
-            _need_rows(ins[i], name, dt, Q.shape, dev)
-        strides += [ins[i].stride(0), ins[i].stride(1)]
         if outs[i] is None:
-            outs[i] = torch.empty(H, N, d, dtype=dt, device=dev)
-        else:
-            _need(outs[i], name + "_out", dt, dev)
-            if outs[i].shape != Q.shape:
-                raise ValueError(f"{name}_out must have the shape [H, N, d] of Q")
-    for name, w, x in (("q_weight", q_weight, Q), ("k_weight", k_weight, K)):
-        if w is not None:
-            _need(w, name, torch.float32, dev)
-            if w.shape != (d,) or x is None:
-                raise ValueError(f"{name} must have the shape [d] and its tensor be given")
-    pairs, naxes, counts, f32 = 0, 0, None, 0
+            outs[i] = torch.empty(shape, dtype=dt, device=dev)
+        elif outs[i].shape != shape:
+            raise ValueError(f"{'QKV'[i]}_out must have the shape [H, N, d] of Q")
+        ptrs[i] = _check_one(outs[i], "QKV"[i] + "_out", dt, dev, index)
+    f32 = torch.float32
+    wq = wk = None
+    if q_weight is not None:
+        wq = _check_one(q_weight, "q_weight", f32, dev, index)
+        if q_weight.numel() != d:
+            raise ValueError("q_weight must have the shape [d]")
+    if k_weight is not None:
+        wk = _check_one(k_weight, "k_weight", f32, dev, index)
+        if k_weight.numel() != d:
+            raise ValueError("k_weight must have the shape [d]")
+    pairs, naxes, counts, pos, freq, pos_f32 = 0, 0, None, None, None, False
     if inv_freq is not None:
-        _need(inv_freq, "inv_freq", torch.float32, dev)
+        freq = _check_one(inv_freq, "inv_freq", f32, dev, index)
         if positions is None:
             raise ValueError("inv_freq needs positions")
-        _need(positions, "positions", (torch.int32, torch.float32), dev)
-        pairs = inv_freq.numel()
-        naxes = positions.shape[1] if positions.dim() == 2 else 1
+        pos_f32 = positions.dtype is f32
+        pos = _check_one(positions, "positions", f32 if pos_f32 else torch.int32, dev, index)
+        pairs, naxes = inv_freq.numel(), 1 if positions.dim() == 1 else positions.shape[-1]
         if positions.dim() not in (1, 2) or positions.shape[0] != N:
             raise ValueError("positions must have the shape [N, axes]")
-        axis_pairs = [pairs] if axis_pairs is None else axis_pairs
+        axis_pairs = (pairs,) if axis_pairs is None else axis_pairs
         if len(axis_pairs) != naxes or sum(axis_pairs) != pairs:
             raise ValueError("axis_pairs must give every axis of positions its pairs of inv_freq")
         counts = (ctypes.c_int32 * naxes)(*axis_pairs)
-        f32 = int(positions.dtype == torch.float32)
     elif positions is not None or axis_pairs is not None:
         raise ValueError("positions and axis_pairs need inv_freq")
-    with _on(dev):
-        st = lib().spark_qk_norm_rope(
-            _ptr(Q), _ptr(K), _ptr(V), _code(dt), H, N, d, (ctypes.c_int64 * 6)(*strides),
-            _ptr(q_weight), _ptr(k_weight), float(eps), _ptr(positions), f32, naxes, counts, pairs,
-            _ptr(inv_freq), int(bool(interleaved)), float(rope_scale), _ptr(outs[0]),
-            _ptr(outs[1]), _ptr(outs[2]), _stream_of(dev, stream))
+    with _on(index):
+        st = lib().spark_qk_norm_rope(q, k or None, v or None, code, H, N, d,
+                                      _Strides(qh, qt, kh, kt, vh, vt), wq, wk, eps, pos, pos_f32,
+                                      naxes, counts, pairs, freq, bool(interleaved), rope_scale,
+                                      *ptrs, _stream_of(index, stream))
     _check("spark_qk_norm_rope", st)
     return tuple(outs)
 
@@ -983,25 +1003,30 @@ def spark_attend_ranges(nq, q_offsets, k_offsets=None, c_offsets=None, prefix=No
     """Key ranges [nq, 4] int32 of packed segments' query rows, from int32 offsets [segments + 1]
     of their queries, video keys and context keys; causal ends a row's context range behind its
     own place or the segment's prefix."""
-    _need(q_offsets, "q_offsets", torch.int32)
+    i32 = torch.int32
+    _need(q_offsets, "q_offsets", i32)
     dev, n = q_offsets.device, q_offsets.numel()
+    index = dev.index
+    ptrs = []
     for name, t, size in (("k_offsets", k_offsets, n), ("c_offsets", c_offsets, n),
                           ("prefix", prefix, n - 1)):
-        if t is not None:
-            _need(t, name, torch.int32, dev)
-            if t.numel() != size:
-                raise ValueError(f"{name} must hold {size} values")
+        if t is None:
+            ptrs.append(None)
+            continue
+        ptrs.append(_check_one(t, name, i32, dev, index))
+        if t.numel() != size:
+            raise ValueError(f"{name} must hold {size} values")
     if prefix is not None and not causal:
         raise ValueError("prefix needs causal")
     if ranges is None:
-        ranges = torch.empty(max(int(nq), 0), 4, dtype=torch.int32, device=dev)
-    _need(ranges, "ranges", torch.int32, dev)
+        ranges = torch.empty(max(int(nq), 0), 4, dtype=i32, device=dev)
+    out = _check_one(ranges, "ranges", i32, dev, index)
     if ranges.shape != (nq, 4):
         raise ValueError("ranges must have the shape [nq, 4]")
-    with _on(dev):
-        st = lib().spark_attend_ranges(int(nq), n - 1, _ptr(q_offsets), _ptr(k_offsets),
-                                       _ptr(c_offsets), _ptr(prefix), int(bool(causal)),
-                                       _ptr(ranges), _ptr(err), _stream_of(dev, stream))
+    flags = None if err is None else _check_one(err, "err", i32, dev, index)
+    with _on(index):
+        st = lib().spark_attend_ranges(nq, n - 1, q_offsets.data_ptr(), *ptrs, bool(causal), out,
+                                       flags, _stream_of(index, stream))
     _check("spark_attend_ranges", st)
     return ranges
 
@@ -1015,41 +1040,45 @@ def spark_attend_dense(Q, K, V, Kc=None, Vc=None, ranges=None, out_dtype=torch.b
     """Dense attention of the rows of Q [H, nq, d] over the video keys K, V [H, nk, d] and the
     context keys Kc, Vc [H, nc, d] (bf16), each row over its ranges ([nq, 4] int32, None: all);
     returns (out, lse)."""
-    bf = torch.bfloat16
+    bf, i32 = torch.bfloat16, torch.int32
     _need(Q, "Q", bf)
     dev = Q.device
+    index = dev.index
     if Q.dim() != 3:
         raise ValueError("Q must have the shape [H, nq, d]")
-    H, nq, d = Q.shape
-    for name, t in (("K", K), ("V", V)):
-        _need(t, name, bf, dev)
+    H, nq, d = shape = Q.shape
+    k, v = _check_one(K, "K", bf, dev, index), _check_one(V, "V", bf, dev, index)
     if K.dim() != 3 or K.shape[0] != H or K.shape[2] != d or V.shape != K.shape:
         raise ValueError("K and V must have the shape [H, nk, d]")
-    Kc, Vc, nc = _context_args(Kc, Vc, H, d, bf, dev)
-    nk = K.shape[1]
+    nk, nc, kc, vc = K.shape[1], 0, None, None
+    if Kc is not None or Vc is not None:
+        kc, vc = _check_one(Kc, "Kc", bf, dev, index), _check_one(Vc, "Vc", bf, dev, index)
+        if Kc.dim() != 3 or Kc.shape[0] != H or Kc.shape[2] != d or Vc.shape != Kc.shape:
+            raise ValueError("Kc and Vc must have the shape [H, nc, d]")
+        nc = Kc.shape[1]
+    rg = None
     if ranges is not None:
-        _need(ranges, "ranges", torch.int32, dev)
+        rg = _check_one(ranges, "ranges", i32, dev, index)
         if ranges.shape != (nq, 4):
             raise ValueError("ranges must have the shape [nq, 4]")
     if out is None:
-        out = torch.empty(H, nq, d, dtype=out_dtype, device=dev)
-    _need(out, "out", (bf, torch.float32), dev)
+        out = torch.empty(shape, dtype=out_dtype, device=dev)
+    code = _code(out.dtype)
+    o = _check_one(out, "out", out.dtype, dev, index)
     if lse is None:
         lse = torch.empty(H, nq, dtype=torch.float32, device=dev)
-    _need(lse, "lse", torch.float32, dev)
-    if out.shape != Q.shape or lse.shape != (H, nq):
+    m = _check_one(lse, "lse", torch.float32, dev, index)
+    if out.shape != shape or lse.shape != (H, nq):
         raise ValueError("out and lse must have the shapes [H, nq, d] and [H, nq]")
     if workspace is None:
         workspace = torch.empty(spark_attend_dense_workspace_size(H, nq, nk, nc, d),
                                 dtype=torch.uint8, device=dev)
-    _need(workspace, "workspace", torch.uint8, dev)
-    if err is not None:
-        _need(err, "err", torch.int32, dev)
-    with _on(dev):
-        st = lib().spark_attend_dense(_ptr(Q), _ptr(K), _ptr(V), _ptr(Kc), _ptr(Vc), H, nq, nk,
-                                      nc, d, _ptr(ranges), _ptr(out), _code(out.dtype), _ptr(lse),
-                                      _ptr(workspace), workspace.numel(), _ptr(err),
-                                      _stream_of(dev, stream))
+    ws = _check_one(workspace, "workspace", torch.uint8, dev, index)
+    flags = None if err is None else _check_one(err, "err", i32, dev, index)
+    with _on(index):
+        st = lib().spark_attend_dense(Q.data_ptr(), k, v, kc, vc, H, nq, nk, nc, d, rg,
+                                      o, code, m, ws, workspace.numel(), flags,
+                                      _stream_of(index, stream))
     _check("spark_attend_dense", st)
     return out, lse
 
@@ -1093,11 +1122,11 @@ def spark_bsa_forward_joint(Q, K, V, Qc, Kc, Vc, q_perm, k_perm, q_offsets, k_of
         size = spark_bsa_workspace_size_joint(H, N, d, nqb, nkb, topk_ratio, nc)
         workspace = torch.empty(size, dtype=torch.uint8, device=dev)
     _need(workspace, "workspace", torch.uint8, dev)
-    with _on(dev):
+    with _on(dev.index):
         st = lib().spark_bsa_forward_joint(
             _ptr(Q), _ptr(K), _ptr(V), _ptr(Qc), _ptr(Kc), _ptr(Vc), nc, _code(Q.dtype), H, N, d,
             _ptr(q_perm), _ptr(k_perm), _ptr(q_offsets), nqb, _ptr(k_offsets), nkb,
             float(topk_ratio), _ptr(out), _ptr(out_c), _ptr(workspace), workspace.numel(),
-            _stream_of(dev, stream))
+            _stream_of(dev.index, stream))
     _check("spark_bsa_forward_joint", st)
     return out, out_c, workspace, layout

@@ -29,6 +29,7 @@
 //
 // Every wait is bounded (see spark_ptx.cuh); on expiry the kernel flags kErrTimeout, drains its
 // copies and MMAs, frees TMEM and returns.
+#include <atomic>
 #include <climits>
 #include <type_traits>
 
@@ -708,14 +709,24 @@ static cudaError_t launch_dense_t(const DenseMaps& m, int H, int nq, int nk, int
                                   cudaStream_t s) {
   auto kern = attend_dense_kernel<D, kPair>;
   constexpr size_t smem = Cfg<D, kPair>::kSmem;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(smem));
+  // The kernel's attributes are set once per device (bit per device; every thread that finds the
+  // bit clear sets the same values).
+  static std::atomic<uint64_t> ready{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  // the register split waits for registers that a launch with fewer would not have
-  cudaFuncAttributes attr;
-  e = cudaFuncGetAttributes(&attr, kern);
-  if (e != cudaSuccess) return e;
-  if (attr.numRegs != kRegsLaunch) return cudaErrorInvalidKernelImage;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (bit == 0 || !(ready.load(std::memory_order_acquire) & bit)) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+    // the register split waits for registers that a launch with fewer would not have
+    cudaFuncAttributes attr;
+    e = cudaFuncGetAttributes(&attr, kern);
+    if (e != cudaSuccess) return e;
+    if (attr.numRegs != kRegsLaunch) return cudaErrorInvalidKernelImage;
+    ready.fetch_or(bit, std::memory_order_release);
+  }
   const dim3 grid(kPair ? (nq + 255) / 256 : 1, nsplit, H);
   kern<<<grid, kThreads, smem, s>>>(m.q, m.k, m.v, m.kc, m.vc, nq, nk, nc,
                                     reinterpret_cast<const int4*>(ranges), nsplit, out, out_dtype,
