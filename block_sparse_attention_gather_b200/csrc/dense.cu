@@ -14,18 +14,19 @@
 // accuracy, so a reference below the true maximum costs none, and the usual tile needs no
 // maximum at all.  The scores stay in TMEM until the sum is known, so the tile can be redone.
 //
-// One CTA works on one head, one slice of the key tiles, and
-//   kPair:  two 128-row query tiles, one per softmax group; every K and V tile serves both;
-//   !kPair: one 128-row query tile; the groups take the even and the odd key tiles, each with
-//           its own O, and the epilogue joins them.
-// 12 warps: 0-3 / 4-7 the softmax groups (warp w owns TMEM lanes 32*(w%4)..), 8 the TMA
-// producer, 9 the MMA issuer, 10 the watch of the loaded tiles.  TMEM columns: S_g at 128 g (P_g written over it as bf16), O_g at
-// 256 + D g.  The next S of a group is issued behind the PV that reads its P, so the commit that
-// announces S(t+1) also tells that PV(t) is complete and O may be rescaled.
+// One CTA works on one head, one 128-row query tile and one slice of the key tiles.  12 warps:
+// 0-3 / 4-7 the softmax groups, which take the even and the odd key tiles (warp w owns TMEM lanes
+// 32*(w%4)..), 8 the TMA producer, 9 the MMA issuer, 10 the watch of the loaded tiles.  TMEM
+// columns: three S buffers (P is written over S as bf16) and one O for both groups.  S(t + 3) is
+// issued behind the PV that reads P(t) in the same buffer, so a group finds the next S of its
+// own waiting when it has handed a tile over, and the commit that announces S(t + 3) also tells
+// that PV(t) is complete.  The groups hand their tiles over in turn (tile t after tile t - 1):
+// only then does a group look at the rows' common reference, which the other may have raised,
+// and raise it itself.
 //
 // Keys beyond a row's ranges are masked to -inf by value, so what they hold (NaN included) does
-// not matter; rows of V outside the ranges of the whole query tile pair are zeroed in shared
-// memory before the product, as 0 * NaN would not be 0.
+// not matter; rows of V outside the ranges of the whole query tile are zeroed in shared memory
+// before the product, as 0 * NaN would not be 0.
 //
 // Every wait is bounded (see spark_ptx.cuh); on expiry the kernel flags kErrTimeout, drains its
 // copies and MMAs, frees TMEM and returns.
@@ -45,24 +46,23 @@ constexpr int kThreads = 384;                // three warpgroups; warp 11 only g
 // warpgroup to the softmax ones; 2 * kRegsSoftmax + kRegsOther == 3 * kRegsLaunch.
 constexpr int kRegsLaunch = 168, kRegsSoftmax = 208, kRegsOther = 88;
 static_assert(2 * kRegsSoftmax + kRegsOther == 3 * kRegsLaunch, "register split");
+constexpr uint32_t kColO = 384;              // S/P buffers at TMEM columns 0, 128, 256
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kMaxSum = 0x1p24f;           // a tile's sum of p from which the reference is raised
 constexpr int kMaxSplits = 64;
 constexpr int kPolyEvery = 4;                // one pair of exponentials in 4 by the polynomial
 
-template <int D, bool kPair>
+template <int D>
 struct Cfg {
   static constexpr int kTile = 128 * D * 2;                  // bytes of one Q, K or V tile
-  static constexpr int kQTiles = kPair ? 2 : 1;
-  // what 227 KB hold next to the query tiles (d = 64: as deep as d = 128 in bytes)
-  static constexpr int kStages = (D == 128 ? 1 : 2) * (kPair ? 5 : 6);
-  static constexpr size_t kSmem = 1024 + static_cast<size_t>(kQTiles + kStages) * kTile;
+  static constexpr int kStages = D == 128 ? 6 : 12;          // what 227 KB hold next to Q
+  static constexpr size_t kSmem = 1024 + static_cast<size_t>(1 + kStages) * kTile;
 };
 
 template <int kStages>
 struct __align__(8) Bars {
-  uint64_t qfull, full[kStages], empty[kStages], sfull[2], pready[2], done;
+  uint64_t qfull, full[kStages], empty[kStages], sfull[3], pready[3], done;
   uint32_t tmem;
   int abort_flag;
 };
@@ -143,16 +143,10 @@ __device__ __forceinline__ void ex2_poly2(uint64_t a2, float& p0, float& p1) {
   p1 = __int_as_float(__float_as_int(y1) + (__float_as_int(r1) << 23));
 }
 
-// Order of the tiles in the shared-memory ring: the order in which the MMA warp first uses them.
-//   kPair:  K0 V0 K1 V1 ...;   otherwise  K0 K1 V0 K2 V1 ... K(T-1) V(T-2) V(T-1).
-template <bool kPair>
-__device__ __forceinline__ int slot_k(int t) {
-  return kPair ? 2 * t : max(2 * t - 1, 0);
-}
-template <bool kPair>
-__device__ __forceinline__ int slot_v(int t, int T) {
-  return kPair ? 2 * t + 1 : min(2 * t + 2, 2 * T - 1);
-}
+// Order of the tiles in the shared-memory ring, that of their first use by the MMA warp:
+// K0 K1 K2 V0 K3 V1 K4 ... K(T-1) V(T-4) V(T-3) V(T-2) V(T-1).
+__device__ __forceinline__ int slot_k(int t) { return t < 3 ? t : 2 * t - 2; }
+__device__ __forceinline__ int slot_v(int t, int T) { return min(2 * t + 3, T + t); }
 
 // 32 columns of this thread's TMEM row without waiting; tmem_wait32 completes it (the registers
 // pass through the wait, so that no use moves before it).
@@ -261,7 +255,7 @@ __device__ __forceinline__ float max_tile(uint32_t sbuf, int lo, int hi) {
 
 }  // namespace
 
-template <int D, bool kPair>
+template <int D>
 __global__ void __launch_bounds__(kThreads, 1) attend_dense_kernel(
     const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
     const __grid_constant__ CUtensorMap map_v, const __grid_constant__ CUtensorMap map_kc,
@@ -269,33 +263,31 @@ __global__ void __launch_bounds__(kThreads, 1) attend_dense_kernel(
     const int4* __restrict__ ranges, int nsplit, void* __restrict__ out, int out_dtype,
     float* __restrict__ lse, float* __restrict__ part, float2* __restrict__ part_ml,
     uint32_t* err, uint64_t wait_ns) {
-  using C = Cfg<D, kPair>;
+  using C = Cfg<D>;
   constexpr int kStages = C::kStages;
   constexpr int kAtoms = D / 64;
-  constexpr int kAhead = kPair ? 1 : 2;                   // tiles from one of a group to its next
   constexpr uint32_t kAll = 0xffffffffu;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   uint8_t* qst = smem;
-  uint8_t* ring = qst + C::kQTiles * C::kTile;
+  uint8_t* ring = qst + C::kTile;
   __shared__ Bars<kStages> bars;
   __shared__ int s_skip;
   __shared__ int hull[8][4];
-  // [group][row] references and sums, over the query tile once every MMA has read it
-  float(*ex_m)[128] = reinterpret_cast<float(*)[128]>(qst);
-  float(*ex_l)[128] = reinterpret_cast<float(*)[128]>(qst + 1024);
+  __shared__ float row_ref[128];             // the rows' reference as of the last tile handed over
+  // sums of the groups' rows, over the query tile once every MMA has read it
+  float(*ex_l)[128] = reinterpret_cast<float(*)[128]>(qst);
   volatile int* abort_flag = &bars.abort_flag;
 
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   const int h = blockIdx.z, split = blockIdx.y;
-  const int q0 = blockIdx.x * (kPair ? 256 : 128);
-  const int groups = !kPair || q0 + 128 < nq ? 2 : 1;     // a pair's second query tile may be void
+  const int q0 = blockIdx.x * 128;
 
   // This thread's row and its key ranges; rows past nq count as unmasked and are never stored.
   const int grp = (warp >> 2) & 1, q4 = warp & 3;
   const int row = q4 * 32 + lane;
-  const int qi = q0 + (kPair ? grp * 128 : 0) + row;
+  const int qi = q0 + row;
   const bool live = warp < 8 && qi < nq;
   int4 rg = make_int4(0, INT_MAX, 0, INT_MAX);
   if (warp < 8) {
@@ -310,6 +302,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_dense_kernel(
     const int a = __reduce_min_sync(kAll, r.x), b = __reduce_max_sync(kAll, r.y);
     const int c = __reduce_min_sync(kAll, r.z), e = __reduce_max_sync(kAll, r.w);
     if (lane == 0) hull[warp][0] = a, hull[warp][1] = b, hull[warp][2] = c, hull[warp][3] = e;
+    if (grp == 0) row_ref[row] = -INFINITY;
   }
   if (tid == 0) {
     s_skip = launch_timed_out(err) ? 1 : 0;               // an earlier CTA gave up
@@ -319,9 +312,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_dense_kernel(
       mbar_init(&bars.full[s], 1);
       mbar_init(&bars.empty[s], 1);
     }
-    for (int g = 0; g < 2; ++g) {
-      mbar_init(&bars.sfull[g], 1);
-      mbar_init(&bars.pready[g], 128 + 1);                // the group's rows and the tiles
+    for (int b = 0; b < 3; ++b) {
+      mbar_init(&bars.sfull[b], 1);
+      mbar_init(&bars.pready[b], 128 + 1);                // the group's rows and the tiles
     }
     mbar_init(&bars.done, 1);
     mbar_fence_init();
@@ -340,7 +333,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_dense_kernel(
   }
   Tiles tl{INT_MAX, 0, INT_MAX, 0, 0, 0, 0};
 #pragma unroll
-  for (int w = 0; w < 8; ++w) {
+  for (int w = 0; w < 4; ++w) {
     tl.vb = min(tl.vb, hull[w][0]), tl.ve = max(tl.ve, hull[w][1]);
     tl.cb = min(tl.cb, hull[w][2]), tl.ce = max(tl.ce, hull[w][3]);
   }
@@ -351,158 +344,161 @@ __global__ void __launch_bounds__(kThreads, 1) attend_dense_kernel(
     tl.count = static_cast<int>(n * (split + 1) / nsplit) - tl.first;
   }
   const int T = tl.count;
+  // waits of a whole warp for a tile's slot, its S, its P
+  auto wait_slot = [&](int i) {
+    return wait_warp(&bars.full[i % kStages], (i / kStages) & 1, abort_flag, err, wait_ns);
+  };
+  auto wait_s = [&](int t) {
+    return wait_warp(&bars.sfull[t % 3], (t / 3) & 1, abort_flag, err, wait_ns);
+  };
+  auto wait_p = [&](int t) {
+    return wait_warp(&bars.pready[t % 3], (t / 3) & 1, abort_flag, err, wait_ns);
+  };
 
   if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
-  if (warp == kWarpLoad) {
-    // -------------------------------------------------------------------- TMA producer
-    int issued = 0;
-    if (T > 0) {
-      if (elect_one()) {
-        tma_prefetch_desc(&map_k);
-        tma_prefetch_desc(&map_v);
-        const int qtiles = kPair ? groups : 1;
-        mbar_arrive_expect_tx(&bars.qfull, qtiles * C::kTile);
-        for (int g = 0; g < qtiles; ++g)
-          for (int a = 0; a < kAtoms; ++a)
-            tma_load_3d(qst + g * C::kTile + a * 16384, &map_q, &bars.qfull, a * 64,
-                        q0 + g * 128, h);
-      }
-      __syncwarp();
-      int nk_done = 0, nv_done = 0;                        // K and V tiles issued
-      for (int i = 0; i < 2 * T; ++i) {
-        const bool is_k = nk_done < T && slot_k<kPair>(nk_done) == i;
-        const int t = is_k ? nk_done++ : nv_done++;
-        const int s = i % kStages;
-        if (i >= kStages &&
-            !wait_warp(&bars.empty[s], ((i / kStages) - 1) & 1, abort_flag, err, wait_ns))
-          break;
+    if (warp == kWarpLoad) {
+      // ------------------------------------------------------------------ TMA producer
+      int issued = 0;
+      if (T > 0) {
         if (elect_one()) {
-          mbar_arrive_expect_tx(&bars.full[s], C::kTile);
-          const CUtensorMap* m = tl.video(t) ? (is_k ? &map_k : &map_v)
-                                             : (is_k ? &map_kc : &map_vc);
+          tma_prefetch_desc(&map_k);
+          tma_prefetch_desc(&map_v);
+          mbar_arrive_expect_tx(&bars.qfull, C::kTile);
           for (int a = 0; a < kAtoms; ++a)
-            tma_load_3d(ring + s * C::kTile + a * 16384, m, &bars.full[s], a * 64, tl.row(t), h);
+            tma_load_3d(qst + a * 16384, &map_q, &bars.qfull, a * 64, q0, h);
         }
         __syncwarp();
-        issued = i + 1;
+        int nk_done = 0, nv_done = 0;                      // K and V tiles issued
+        for (int i = 0; i < 2 * T; ++i) {
+          const bool is_k = nk_done < T && slot_k(nk_done) == i;
+          const int t = is_k ? nk_done++ : nv_done++;
+          const int s = i % kStages;
+          if (i >= kStages &&
+              !wait_warp(&bars.empty[s], ((i / kStages) - 1) & 1, abort_flag, err, wait_ns))
+            break;
+          if (elect_one()) {
+            mbar_arrive_expect_tx(&bars.full[s], C::kTile);
+            const CUtensorMap* m = tl.video(t) ? (is_k ? &map_k : &map_v)
+                                               : (is_k ? &map_kc : &map_vc);
+            for (int a = 0; a < kAtoms; ++a)
+              tma_load_3d(ring + s * C::kTile + a * 16384, m, &bars.full[s], a * 64, tl.row(t), h);
+          }
+          __syncwarp();
+          issued = i + 1;
+        }
+        // every load has landed before the CTA ends (after an abort some were never consumed)
+        for (int i = max(0, issued - kStages); i < issued; ++i)
+          drain(&bars.full[i % kStages], (i / kStages) & 1);
+        drain(&bars.qfull, 0);
       }
-      // every load has landed before the CTA ends (after an abort some were never consumed)
-      for (int i = max(0, issued - kStages); i < issued; ++i)
-        drain(&bars.full[i % kStages], (i / kStages) & 1);
-      drain(&bars.qfull, 0);
-    }
-  } else if (warp == kWarpMma) {
-    // ---------------------------------------------------------------------- MMA issuer
-    // Per tile and group one wait, for P and what the tile warp has seen land, then O += P V and
-    // the group's next S over that P back to back.
-    constexpr uint32_t idS = idesc_bf16(128, 128, false, false);
-    constexpr uint32_t idO = idesc_bf16(128, D, false, true);
-    const uint64_t qd = sdesc_sw128(smem_u32(qst), 16, 1024);
-    const uint64_t kd0 = sdesc_sw128(smem_u32(ring), 16, 1024);
-    const uint64_t vd0 = sdesc_sw128(smem_u32(ring), 16384, 1024);
-    // one lane: the group's S of key tile t; the tile's last reader frees its stage
-    auto mma_s = [&](int t, int g) {
-      const int i = slot_k<kPair>(t);
-      const uint64_t kd = kd0 + static_cast<uint64_t>((i % kStages) * (C::kTile >> 4));
-      const uint64_t q = qd + static_cast<uint64_t>(kPair ? g * (C::kTile >> 4) : 0);
+    } else if (warp == kWarpMma) {
+      // -------------------------------------------------------------------- MMA issuer
+      // S(0), S(1), S(2), then per tile O += P V(t) and S(t + 3) over that P (MMAs of one thread
+      // execute in order).  One wait a tile, for P and what the tile watch has seen land.
+      constexpr uint32_t idS = idesc_bf16(128, 128, false, false);
+      constexpr uint32_t idO = idesc_bf16(128, D, false, true);
+      const uint64_t qd = sdesc_sw128(smem_u32(qst), 16, 1024);
+      const uint64_t kd0 = sdesc_sw128(smem_u32(ring), 16, 1024);
+      const uint64_t vd0 = sdesc_sw128(smem_u32(ring), 16384, 1024);
+      auto mma_s = [&](int t) {                            // one lane
+        const int i = slot_k(t);
+        const uint64_t kd = kd0 + static_cast<uint64_t>((i % kStages) * (C::kTile >> 4));
 #pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk) {
-        const uint32_t off = ((kk / 4) * 16384 + (kk % 4) * 32) / 16;
-        mma_ss(tbase + g * 128, q + off, kd + off, idS, kk > 0 ? 1u : 0u);
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t off = ((kk / 4) * 16384 + (kk % 4) * 32) / 16;
+          mma_ss(tbase + (t % 3) * 128, qd + off, kd + off, idS, kk > 0 ? 1u : 0u);
+        }
+        tc_commit(&bars.empty[i % kStages]);
+      };
+      bool ok = T > 0 && wait_warp(&bars.qfull, 0, abort_flag, err, wait_ns);
+      for (int t = 0; ok && t < min(T, 3); ++t) {
+        if (!(ok = wait_slot(slot_k(t)))) break;
+        if (elect_one()) {
+          mma_s(t);
+          tc_commit(&bars.sfull[t]);
+        }
+        __syncwarp();
       }
-      tc_commit(&bars.sfull[g]);
-      if (!kPair || g + 1 == groups) tc_commit(&bars.empty[i % kStages]);
-    };
-    // one lane: O_g += P V of key tile t, `first` the group's first
-    auto mma_pv = [&](int t, int g, bool first) {
-      const int i = slot_v<kPair>(t, T);
-      const uint64_t vd = vd0 + static_cast<uint64_t>((i % kStages) * (C::kTile >> 4));
-#pragma unroll
-      for (int kk = 0; kk < 8; ++kk)
-        mma_ts(tbase + 256 + g * D, tbase + g * 128 + kk * 8, vd + (kk * 2048) / 16, idO,
-               (kk > 0 || !first) ? 1u : 0u);
-      if (!kPair || g + 1 == groups) tc_commit(&bars.empty[i % kStages]);
-    };
-    auto wait_full = [&](int i) {
-      return wait_warp(&bars.full[i % kStages], (i / kStages) & 1, abort_flag, err, wait_ns);
-    };
-    bool ok = T > 0 && wait_warp(&bars.qfull, 0, abort_flag, err, wait_ns);
-    for (int t = 0; ok && t < (kPair ? 1 : min(T, 2)); ++t) {
-      if (!(ok = wait_full(slot_k<kPair>(t)))) break;
-      if (elect_one())
-        for (int g = kPair ? 0 : t; g < (kPair ? groups : t + 1); ++g) mma_s(t, g);
-      __syncwarp();
-    }
-    for (int t = 0; ok && t < T; ++t) {
-      const bool more = t + kAhead < T;
-      for (int g = kPair ? 0 : t & 1; g < (kPair ? groups : (t & 1) + 1); ++g) {
-        ok = wait_warp(&bars.pready[g], (kPair ? t : t >> 1) & 1, abort_flag, err, wait_ns);
-        if (!ok) break;
+      for (int t = 0; ok && t < T; ++t) {
+        if (!(ok = wait_p(t))) break;
         tc_fence_after_sync();
         if (elect_one()) {
-          mma_pv(t, g, kPair ? t == 0 : t < 2);
-          if (more) mma_s(t + kAhead, g);
+          const int i = slot_v(t, T);
+          const uint64_t vd = vd0 + static_cast<uint64_t>((i % kStages) * (C::kTile >> 4));
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            mma_ts(tbase + kColO, tbase + (t % 3) * 128 + kk * 8, vd + (kk * 2048) / 16, idO,
+                   (kk > 0 || t > 0) ? 1u : 0u);
+          tc_commit(&bars.empty[i % kStages]);
+          if (t + 3 < T) mma_s(t + 3);
+          tc_commit(&bars.sfull[t % 3]);                   // S(t + 3) is there, PV(t) complete
         }
         __syncwarp();
       }
-    }
-    // every MMA complete: the epilogue reads O, and TMEM is freed after
-    if (elect_one()) tc_commit(&bars.done);
-    __syncwarp();
-    drain(&bars.done, 0);
-  } else if (warp == kWarpTiles) {
-    // ---------------------------------------------------------------------- tile watch
-    // Waits for the V tile and the group's next K tile in the MMA warp's stead and arrives at
-    // pready for them: a barrier test takes a few hundred cycles while the MMAs read shared
-    // memory, and the MMA warp's are all in the way.
-    for (int t = 0; t < T; ++t) {
-      const int i = slot_v<kPair>(t, T), j = slot_k<kPair>(t + kAhead);
-      bool ok = wait_warp(&bars.full[i % kStages], (i / kStages) & 1, abort_flag, err, wait_ns);
-      if (ok && t + kAhead < T)
-        ok = wait_warp(&bars.full[j % kStages], (j / kStages) & 1, abort_flag, err, wait_ns);
-      for (int g = kPair ? 0 : t & 1; ok && g < (kPair ? groups : (t & 1) + 1); ++g) {
-        const int n = kPair ? t : t >> 1;
+      // every MMA complete: the epilogue reads O, and TMEM is freed after
+      if (elect_one()) tc_commit(&bars.done);
+      __syncwarp();
+      drain(&bars.done, 0);
+    } else if (warp == kWarpTiles) {
+      // -------------------------------------------------------------------- tile watch
+      // Waits for V(t) and K(t + 3) in the MMA warp's stead and arrives at pready for them: a
+      // barrier test takes a few hundred cycles while the MMAs read shared memory, and the MMA
+      // warp's are all in the way.
+      for (int t = 0; t < T; ++t) {
+        if (!wait_slot(slot_v(t, T)) || (t + 3 < T && !wait_slot(slot_k(t + 3)))) break;
         // the phase before has to be over, or this would count for it
-        if (n > 0) ok = wait_warp(&bars.pready[g], (n - 1) & 1, abort_flag, err, wait_ns);
-        if (ok && elect_one()) mbar_arrive(&bars.pready[g]);
+        if (t >= 3 && !wait_p(t - 3)) break;
+        if (elect_one()) mbar_arrive(&bars.pready[t % 3]);
         __syncwarp();
       }
-      if (!ok) break;
     }
-  }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
     // -------------------------------------------------------------------- softmax rows
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
     const uint32_t lane_off = static_cast<uint32_t>(q4 * 32) << 16;
-    const uint32_t obuf = tbase + lane_off + 256 + grp * D;
+    const uint32_t obuf = tbase + lane_off + kColO;
     const float c = kLog2e * rsqrtf(static_cast<float>(D));
     const bool warp_live = __any_sync(kAll, live);         // else nothing of this warp is stored
-    float ref = -INFINITY, l = 0.f;                        // log2 units; sum of 2^(. - ref)
-    const uint32_t sbuf = tbase + lane_off + grp * 128;
-    const int ntiles = kPair ? (grp < groups ? T : 0) : (T + 1 - grp) / 2;
+    float ref = -INFINITY, l = 0.f;                        // log2 units; the group's sum of p
     bool ok = true;
-    for (int n = 0; n < ntiles; ++n) {
-      const int t = kPair ? n : 2 * n + grp;
-      ok = wait_warp(&bars.sfull[grp], n & 1, abort_flag, err, wait_ns);
-      if (!ok) break;
+    for (int t = grp; t < T; t += 2) {
+      if (!(ok = wait_s(t))) break;
       tc_fence_after_sync();
+      const uint32_t sbuf = tbase + lane_off + (t % 3) * 128;
       const int y = tl.row(t);
       const bool video = tl.video(t);
-      if (warp_live) {
-        const int lo = (video ? rg.x : rg.z) - y, hi = (video ? rg.y : rg.w) - y;
+      const int lo = (video ? rg.x : rg.z) - y, hi = (video ? rg.y : rg.w) - y;
+      const bool some = max(lo, 0) < min(hi, 128);
+      uint32_t pk[4][16];
+      if (!__any_sync(kAll, some && warp_live)) {
+        // no row of this warp has a key here: zeros, whatever the reference
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int j = 0; j < 16; ++j) pk[i][j] = 0u;
+      } else {
         const bool edge = __any_sync(kAll, lo > 0 || hi < 128);
-        uint32_t pk[4][16];
-        float sum = 0.f;
-        // a row without a reference that sees its first keys needs the maximum at once
-        bool rise = __any_sync(kAll, ref == -INFINITY && max(lo, 0) < min(hi, 128));
-        if (!rise) {
+        float sum;
+        for (int pass = 0;; ++pass) {
           const float m = ref == -INFINITY ? 0.f : ref;    // no live key yet: every p is 0
-          sum = edge ? exp_tile<true>(sbuf, lo, hi, c, m, pk)
-                     : exp_tile<false>(sbuf, lo, hi, c, m, pk);
-          rise = __any_sync(kAll, !(sum < kMaxSum));
-        }
-        if (rise) {
+          sum = edge || pass > 0 ? exp_tile<true>(sbuf, lo, hi, c, m, pk)
+                                 : exp_tile<false>(sbuf, lo, hi, c, m, pk);
+          if (pass == 0) {
+            // The other group hands its tile over first; it may have raised the reference, which
+            // what is here then has to follow.
+            if (t > 0 && !(ok = wait_p(t - 1))) break;
+            const float cur = row_ref[row];
+            const bool moved = __float_as_uint(cur) != __float_as_uint(ref);
+            if (__any_sync(kAll, moved)) {
+              if (moved) l *= ref == -INFINITY ? 1.f : ex2_approx(ref - cur);
+              ref = cur;
+              continue;
+            }
+          }
+          // the reference is too low, or a row sees its first keys without one
+          if (pass == 2 || !__any_sync(kAll, !(sum < kMaxSum) || (ref == -INFINITY && some)))
+            break;
           const float mx = max_tile(sbuf, lo, hi) * c;
           const bool grow = !(mx <= ref);                  // a NaN among the scores too
           // a score of +inf leaves no number to compare the others with
@@ -510,7 +506,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_dense_kernel(
           const float f = grow ? ex2_approx(ref - next) : 1.f;
           ref = next;
           l *= f;
-          if (n > 0) {
+          if (t > 0) {
+            // PV(t - 1) is complete when the S behind it, or its place, is announced
+            if (!(ok = wait_s(t + 2))) break;
+            tc_fence_after_sync();
 #pragma unroll 1
             for (int cc = 0; cc < D; cc += 16) {
               uint32_t o[16];
@@ -520,21 +519,20 @@ __global__ void __launch_bounds__(kThreads, 1) attend_dense_kernel(
               tmem_st16_issue(obuf + cc, o);
             }
           }
-          sum = exp_tile<true>(sbuf, lo, hi, c, ref == -INFINITY ? 0.f : ref, pk);
+          row_ref[row] = ref;
+          pass = 1;                                        // once more, then it stands
         }
-        l += sum;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) tmem_st16_issue(sbuf + 16 * i, pk[i]);
-        tmem_wait_st();
-      }
-      // V rows past the hull that are not past the tensor (those TMA fills with zeros): zeroed
-      // by group 0, whose P the MMA warp waits for first (kPair), or by the tile's own group
-      const int end = (video ? tl.ve : tl.ce) - y, rows = (video ? nk : nc) - y;
-      const bool zero = end < 128 && end < rows && (!kPair || grp == 0);
-      if (zero) {
-        const int i = slot_v<kPair>(t, T);
-        ok = wait_warp(&bars.full[i % kStages], (i / kStages) & 1, abort_flag, err, wait_ns);
         if (!ok) break;
+        l += sum;
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) tmem_st16_issue(sbuf + 16 * i, pk[i]);
+      tmem_wait_st();
+      // V rows past the hull that are not past the tensor (those TMA fills with zeros)
+      const int end = (video ? tl.ve : tl.ce) - y, rows = (video ? nk : nc) - y;
+      if (end < 128 && end < rows) {
+        const int i = slot_v(t, T);
+        if (!(ok = wait_slot(i))) break;
         uint8_t* v = ring + (i % kStages) * C::kTile;
         for (int a = 0; a < kAtoms; ++a)
           for (int k = end * 8 + row; k < 128 * 8; k += 128)
@@ -542,57 +540,40 @@ __global__ void __launch_bounds__(kThreads, 1) attend_dense_kernel(
         fence_proxy_async_smem();
       }
       tc_fence_before_sync();
-      mbar_arrive(&bars.pready[grp]);
+      mbar_arrive(&bars.pready[t % 3]);
     }
-    // ---- epilogue
+    // ---- epilogue: each group's warps store half of the columns
     if (ok && T > 0)
       ok = wait_warp(&bars.done, 0, abort_flag, err, wait_ns);
-    float w[2] = {1.f, 1.f};                               // weights of the two groups' O
-    bool read0 = true, read1 = false;                      // which hold something
-    if constexpr (!kPair) {
-      ex_m[grp][row] = ref;
-      ex_l[grp][row] = l;
-      named_bar_sync(1 + q4, 64);                          // the two groups of this quarter
-      const float m0 = ex_m[0][row], m1 = ex_m[1][row];
-      ref = fmaxf(m0, m1);
-      w[0] = m0 > -INFINITY ? ex2_approx(m0 - ref) : 0.f;
-      w[1] = m1 > -INFINITY ? ex2_approx(m1 - ref) : 0.f;
-      l = w[0] * ex_l[0][row] + w[1] * ex_l[1][row];
-      read0 = read1 = T > 0;
-    } else {
-      read0 = T > 0;
+    {
+      const float last = row_ref[row];                     // the tiles are all handed over
+      if (__float_as_uint(last) != __float_as_uint(ref))
+        l *= ref == -INFINITY ? 1.f : ex2_approx(ref - last);
+      ref = last;
     }
-    if (ok && warp_live && grp < groups) {
+    ex_l[grp][row] = l;
+    named_bar_sync(1 + q4, 64);                            // the two groups of this quarter
+    l = ex_l[0][row] + ex_l[1][row];
+    if (ok && warp_live) {
       tc_fence_after_sync();
       const size_t at = static_cast<size_t>(h) * nq + qi;
       const size_t prow = (static_cast<size_t>(h) * nsplit + split) * nq + qi;
       // one slice: the output; several: unnormalised partial sums for the join
       const float inv = nsplit > 1 ? 1.f : 1.f / l;
       const bool none = l == 0.f;                          // no live key: zeros
-      constexpr int kCols = kPair ? D : D / 2;             // columns this warp stores
-      const int col0 = kPair ? 0 : grp * kCols;
-      const uint32_t o0 = tbase + lane_off + 256 + (kPair ? grp * D : 0);
 #pragma unroll
-      for (int cc = 0; cc < kCols; cc += 32) {
-        const int col = col0 + cc;
+      for (int cc = 0; cc < D / 2; cc += 32) {
+        const int col = grp * (D / 2) + cc;
         float o[32];
 #pragma unroll
         for (int j = 0; j < 32; ++j) o[j] = 0.f;
-        if (read0) {
+        if (T > 0) {
           uint32_t a[32];
-          tmem_ld32(o0 + col, a);
+          tmem_ld32(obuf + col, a);
 #pragma unroll
-          for (int j = 0; j < 32; ++j) o[j] = w[0] * __uint_as_float(a[j]);
-        }
-        if (read1) {
-          uint32_t a[32];
-          tmem_ld32(o0 + D + col, a);
-#pragma unroll
-          for (int j = 0; j < 32; ++j) o[j] = fmaf(w[1], __uint_as_float(a[j]), o[j]);
+          for (int j = 0; j < 32; ++j) o[j] = none ? 0.f : __uint_as_float(a[j]) * inv;
         }
         if (live) {
-#pragma unroll
-          for (int j = 0; j < 32; ++j) o[j] = none ? 0.f : o[j] * inv;
           if (nsplit > 1 || out_dtype == 1) {
             float4* dst = reinterpret_cast<float4*>(
                 nsplit > 1 ? part + prow * D + col : static_cast<float*>(out) + at * D + col);
@@ -611,7 +592,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_dense_kernel(
           }
         }
       }
-      if (live && (kPair || grp == 0)) {
+      if (live && grp == 0) {
         if (nsplit > 1)
           part_ml[prow] = make_float2(ref, l);
         else if (lse != nullptr)
@@ -673,13 +654,12 @@ __global__ void __launch_bounds__(256) attend_dense_join_kernel(
   if (lane == 0 && lse != nullptr) lse[r] = (m + log2f(l)) * kLn2;
 }
 
-// Slices of the key tiles per query tile (pair): the count with the least estimated time on 148
-// SMs, one CTA each.  A tile is taken as 1 unit (both query tiles of a pair: 2), a CTA's start
-// and end as 4, the join kernel as 5 plus the partial sums' traffic.
+// Slices of the key tiles per query tile: the count with the least estimated time on 148
+// SMs, one CTA each.  A tile is taken as 1 unit, a CTA's start and end as 4, the join kernel as 5 plus the partial sums' traffic.
 int attend_dense_splits(int H, int nq, int nk, int nc, int d) {
   constexpr int kSms = 148;
   const long long qt = (static_cast<long long>(nq) + 127) / 128;
-  const long long units = static_cast<long long>(H) * (qt > 1 ? (qt + 1) / 2 : 1);
+  const long long units = static_cast<long long>(H) * qt;
   const long long T = (static_cast<long long>(nk) + 127) / 128 + (nc + 127) / 128;
   int best = 1;
   double least = 0;
@@ -688,7 +668,7 @@ int attend_dense_splits(int H, int nq, int nk, int nc, int d) {
     const double bytes = static_cast<double>(H) * nq * d * 8.0 * s;
     if (s > 1 && bytes > 512e6) break;
     const double cost = static_cast<double>(waves) *
-                            (static_cast<double>((T + s - 1) / s) * (qt > 1 ? 2 : 1) + 4) +
+                            (static_cast<double>((T + s - 1) / s) + 4) +
                         (s > 1 ? 5 + bytes / 4e6 : 0);
     if (s == 1 || cost < least) least = cost, best = s;
   }
@@ -702,13 +682,13 @@ size_t attend_dense_workspace(int H, int nq, int nk, int nc, int d) {
   return (rows * d * 4 + 255) / 256 * 256 + (rows * 8 + 255) / 256 * 256;
 }
 
-template <int D, bool kPair>
+template <int D>
 static cudaError_t launch_dense_t(const DenseMaps& m, int H, int nq, int nk, int nc,
                                   const int32_t* ranges, int nsplit, void* out, int out_dtype,
                                   float* lse, float* part, float2* ml, uint32_t* err,
                                   cudaStream_t s) {
-  auto kern = attend_dense_kernel<D, kPair>;
-  constexpr size_t smem = Cfg<D, kPair>::kSmem;
+  auto kern = attend_dense_kernel<D>;
+  constexpr size_t smem = Cfg<D>::kSmem;
   // The kernel's attributes are set once per device (bit per device; every thread that finds the
   // bit clear sets the same values).
   static std::atomic<uint64_t> ready{0};
@@ -727,7 +707,7 @@ static cudaError_t launch_dense_t(const DenseMaps& m, int H, int nq, int nk, int
     if (attr.numRegs != kRegsLaunch) return cudaErrorInvalidKernelImage;
     ready.fetch_or(bit, std::memory_order_release);
   }
-  const dim3 grid(kPair ? (nq + 255) / 256 : 1, nsplit, H);
+  const dim3 grid((nq + 127) / 128, nsplit, H);
   kern<<<grid, kThreads, smem, s>>>(m.q, m.k, m.v, m.kc, m.vc, nq, nk, nc,
                                     reinterpret_cast<const int4*>(ranges), nsplit, out, out_dtype,
                                     lse, part, ml, err, wait_limit_ns());
@@ -743,16 +723,10 @@ cudaError_t launch_attend_dense(const DenseMaps& maps, int H, int nq, int nk, in
   const size_t part_bytes = (static_cast<size_t>(rows) * nsplit * d * 4 + 255) / 256 * 256;
   float2* ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + part_bytes);
   cudaError_t e;
-  if (d == 128)
-    e = nq > 128 ? launch_dense_t<128, true>(maps, H, nq, nk, nc, ranges, nsplit, out, out_dtype,
-                                             lse, part, ml, err, s)
-                 : launch_dense_t<128, false>(maps, H, nq, nk, nc, ranges, nsplit, out, out_dtype,
-                                              lse, part, ml, err, s);
-  else
-    e = nq > 128 ? launch_dense_t<64, true>(maps, H, nq, nk, nc, ranges, nsplit, out, out_dtype,
-                                            lse, part, ml, err, s)
-                 : launch_dense_t<64, false>(maps, H, nq, nk, nc, ranges, nsplit, out, out_dtype,
-                                             lse, part, ml, err, s);
+  e = d == 128 ? launch_dense_t<128>(maps, H, nq, nk, nc, ranges, nsplit, out, out_dtype, lse, part,
+                                     ml, err, s)
+               : launch_dense_t<64>(maps, H, nq, nk, nc, ranges, nsplit, out, out_dtype, lse, part,
+                                    ml, err, s);
   if (e != cudaSuccess || nsplit == 1) return e;
   const unsigned grid = static_cast<unsigned>((rows + 7) / 8);
   if (d == 128)
