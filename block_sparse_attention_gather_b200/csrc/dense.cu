@@ -8,7 +8,7 @@
 //
 // One pass over the keys with a running reference per row (an online softmax):
 //   p_j = 2^(s_j log2e - ref),  l = sum p,  O = sum p v,  out = O / l,  lse = (ref + log2 l) ln2.
-// ref is the row's maximum over its first tile with a live key.  It is raised to a later tile's
+// ref is the row's maximum over the first two tiles (the first with a live key).  It is raised to a later tile's
 // maximum, and O and l rescaled, only when that tile's sum of p reaches 2^24 (or is no number):
 // up to there p, rounded to bf16 for the tensor cores, and the fp32 sums keep their relative
 // accuracy, so a reference below the true maximum costs none, and the usual tile needs no
@@ -51,7 +51,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kMaxSum = 0x1p24f;           // a tile's sum of p from which the reference is raised
 constexpr int kMaxSplits = 64;
-constexpr int kPolyEvery = 4;                // one pair of exponentials in 4 by the polynomial
+constexpr int kPolyEvery = 8;                // one pair of exponentials in 8 by the polynomial
 
 template <int D>
 struct Cfg {
@@ -276,6 +276,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_dense_kernel(
   __shared__ int s_skip;
   __shared__ int hull[8][4];
   __shared__ float row_ref[128];             // the rows' reference as of the last tile handed over
+  __shared__ float first_max[2][128];        // the rows' maxima of each group's first tile
   // sums of the groups' rows, over the query tile once every MMA has read it
   float(*ex_l)[128] = reinterpret_cast<float(*)[128]>(qst);
   volatile int* abort_flag = &bars.abort_flag;
@@ -462,7 +463,23 @@ __global__ void __launch_bounds__(kThreads, 1) attend_dense_kernel(
     const bool warp_live = __any_sync(kAll, live);         // else nothing of this warp is stored
     float ref = -INFINITY, l = 0.f;                        // log2 units; the group's sum of p
     bool ok = true;
-    for (int t = grp; t < T; t += 2) {
+    // The reference to start with: the maximum over both groups' first tiles.
+    if (T > 0) {
+      float mx = -INFINITY;
+      if (grp < T && (ok = wait_s(grp)) && warp_live) {
+        tc_fence_after_sync();
+        const int y = tl.row(grp);
+        const bool video = tl.video(grp);
+        mx = c * max_tile(tbase + lane_off + grp * 128, (video ? rg.x : rg.z) - y,
+                          (video ? rg.y : rg.w) - y);
+      }
+      first_max[grp][row] = mx;
+      named_bar_sync(1 + q4, 64);                          // the two groups of this quarter
+      ref = max_nan(first_max[0][row], first_max[1][row]);
+      if (!(ref < INFINITY)) ref = NAN;                    // a score that nothing compares with
+      if (grp == 0) row_ref[row] = ref;
+    }
+    for (int t = grp; ok && t < T; t += 2) {
       if (!(ok = wait_s(t))) break;
       tc_fence_after_sync();
       const uint32_t sbuf = tbase + lane_off + (t % 3) * 128;
@@ -609,35 +626,61 @@ __global__ void __launch_bounds__(kThreads, 1) attend_dense_kernel(
 }
 
 // Joins the slices of a row: out = sum_s 2^(ref_s - ref) O_s / sum_s 2^(ref_s - ref) l_s with
-// ref the largest.  One warp per row; D/32 columns per lane.
+// ref the largest, in the order of the slices.  One warp per row, D/32 columns per lane; the
+// slices' references come a lane each (up to 64), and eight slices' columns are loaded at once:
+// one at a time, the loads' latency took 10 us for 16 slices.
 template <int D>
 __global__ void __launch_bounds__(256) attend_dense_join_kernel(
     const float* __restrict__ part, const float2* __restrict__ part_ml, int nq, int nsplit,
     long long rows, void* __restrict__ out, int out_dtype, float* __restrict__ lse) {
   constexpr int kPer = D / 32;
+  constexpr uint32_t kAll = 0xffffffffu;
+  static_assert(kMaxSplits == 64, "two slices a lane");
+  // the attention kernel's partial sums are there from here on
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const long long r = static_cast<long long>(blockIdx.x) * 8 + threadIdx.x / 32;
   const int lane = threadIdx.x % 32;
   if (r >= rows) return;
   const size_t base = static_cast<size_t>(r / nq) * nsplit * nq + static_cast<size_t>(r % nq);
-  float m = -INFINITY;
-  for (int s = lane; s < nsplit; s += 32) m = fmaxf(m, part_ml[base + static_cast<size_t>(s) * nq].x);
+  float2 ml[2];
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  float l = 0.f, acc[kPer] = {};
-  for (int s = 0; s < nsplit; ++s) {
-    const size_t at = base + static_cast<size_t>(s) * nq;
-    const float2 ml = part_ml[at];
-    if (ml.y == 0.f) continue;                             // a slice without a live key
-    const float w = ex2_approx(ml.x - m);
-    l = fmaf(w, ml.y, l);
-    const float* src = part + at * D + lane * kPer;
-    if constexpr (kPer == 4) {
-      const float4 v = *reinterpret_cast<const float4*>(src);
-      acc[0] = fmaf(w, v.x, acc[0]), acc[1] = fmaf(w, v.y, acc[1]);
-      acc[2] = fmaf(w, v.z, acc[2]), acc[3] = fmaf(w, v.w, acc[3]);
-    } else {
-      const float2 v = *reinterpret_cast<const float2*>(src);
-      acc[0] = fmaf(w, v.x, acc[0]), acc[1] = fmaf(w, v.y, acc[1]);
+  for (int i = 0; i < 2; ++i) {
+    const int s = lane + 32 * i;
+    ml[i] = s < nsplit ? part_ml[base + static_cast<size_t>(s) * nq] : make_float2(-INFINITY, 0.f);
+  }
+  float m = fmaxf(ml[0].x, ml[1].x);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kAll, m, o));
+  float w[2], l = 0.f, acc[kPer] = {};
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    // a slice without a live key has l = 0 and zeros
+    w[i] = ml[i].y == 0.f ? 0.f : ex2_approx(ml[i].x - m);
+    ml[i].y *= w[i];
+  }
+  for (int s0 = 0; s0 < nsplit; s0 += 8) {
+    float v[8][kPer];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int s = min(s0 + j, nsplit - 1);
+      const float* src = part + (base + static_cast<size_t>(s) * nq) * D + lane * kPer;
+      if constexpr (kPer == 4) {
+        const float4 f = *reinterpret_cast<const float4*>(src);
+        v[j][0] = f.x, v[j][1] = f.y, v[j][2] = f.z, v[j][3] = f.w;
+      } else {
+        const float2 f = *reinterpret_cast<const float2*>(src);
+        v[j][0] = f.x, v[j][1] = f.y;
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int s = s0 + j;
+      const float ws = __shfl_sync(kAll, s < 32 ? w[0] : w[1], s & 31);
+      const float ls = __shfl_sync(kAll, s < 32 ? ml[0].y : ml[1].y, s & 31);
+      if (s >= nsplit) break;                              // uniform
+      l += ls;
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) acc[k] = fmaf(ws, v[j][k], acc[k]);
     }
   }
   const float inv = l == 0.f ? 0.f : 1.f / l;
@@ -714,6 +757,25 @@ static cudaError_t launch_dense_t(const DenseMaps& m, int H, int nq, int nk, int
   return cudaGetLastError();
 }
 
+// The join's launch overlaps the attention kernel's end, which it waits for (asking for it any
+// earlier, from the attention kernel's start, measured 8% slower on packed prompts).
+template <int D>
+static cudaError_t launch_join_t(const float* part, const float2* ml, int nq, int nsplit,
+                                 long long rows, void* out, int out_dtype, float* lse,
+                                 cudaStream_t s) {
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>((rows + 7) / 8));
+  cfg.blockDim = dim3(256);
+  cfg.stream = s;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, attend_dense_join_kernel<D>, part, ml, nq, nsplit, rows, out,
+                            out_dtype, lse);
+}
+
 cudaError_t launch_attend_dense(const DenseMaps& maps, int H, int nq, int nk, int nc, int d,
                                 const int32_t* ranges, void* out, int out_dtype, float* lse,
                                 void* workspace, uint32_t* err, cudaStream_t s) {
@@ -728,14 +790,8 @@ cudaError_t launch_attend_dense(const DenseMaps& maps, int H, int nq, int nk, in
                : launch_dense_t<64>(maps, H, nq, nk, nc, ranges, nsplit, out, out_dtype, lse, part,
                                     ml, err, s);
   if (e != cudaSuccess || nsplit == 1) return e;
-  const unsigned grid = static_cast<unsigned>((rows + 7) / 8);
-  if (d == 128)
-    attend_dense_join_kernel<128><<<grid, 256, 0, s>>>(part, ml, nq, nsplit, rows, out, out_dtype,
-                                                       lse);
-  else
-    attend_dense_join_kernel<64><<<grid, 256, 0, s>>>(part, ml, nq, nsplit, rows, out, out_dtype,
-                                                      lse);
-  return cudaGetLastError();
+  return d == 128 ? launch_join_t<128>(part, ml, nq, nsplit, rows, out, out_dtype, lse, s)
+                  : launch_join_t<64>(part, ml, nq, nsplit, rows, out, out_dtype, lse, s);
 }
 
 // ------------------------------------------------------------------------------ key ranges
