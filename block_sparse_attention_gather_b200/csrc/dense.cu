@@ -51,7 +51,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kMaxSum = 0x1p24f;           // a tile's sum of p from which the reference is raised
 constexpr int kMaxSplits = 64;
-constexpr int kPolyEvery = 8;                // one pair of exponentials in 8 by the polynomial
+constexpr int kPolyEvery = 3;                // of 16 pairs of exponentials every third by polynomial
 
 template <int D>
 struct Cfg {
@@ -214,25 +214,25 @@ __device__ __forceinline__ uint64_t exp32(const uint32_t (&r)[32], uint32_t live
 }
 
 // The tile's 128 scores at `sbuf` -> packed pairs, returning the sum of p; columns outside
-// [lo, hi) are masked when kExact.  The load of the next 32 columns is in flight while the
-// current ones are exponentiated.
+// [lo, hi) are masked when kExact.  The load of the second half's columns is in flight while the
+// first half's are exponentiated.
 template <bool kExact>
 __device__ __forceinline__ float exp_tile(uint32_t sbuf, int lo, int hi, float c, float m,
                                           uint32_t (&pk)[4][16]) {
   const uint64_t c2 = f2_splat(c), nm2 = f2_splat(-m);
-  uint32_t ra[32], rb[32];
-  tmem_ld32_issue(sbuf, ra);
-  tmem_wait32(ra);
-  tmem_ld32_issue(sbuf + 32, rb);
-  uint64_t s = exp32<kExact>(ra, kExact ? bits32(lo, hi) : 0u, c2, nm2, pk[0]);
-  tmem_wait32(rb);
-  tmem_ld32_issue(sbuf + 64, ra);
-  s = f2_add(s, exp32<kExact>(rb, kExact ? bits32(lo - 32, hi - 32) : 0u, c2, nm2, pk[1]));
-  tmem_wait32(ra);
-  tmem_ld32_issue(sbuf + 96, rb);
-  s = f2_add(s, exp32<kExact>(ra, kExact ? bits32(lo - 64, hi - 64) : 0u, c2, nm2, pk[2]));
-  tmem_wait32(rb);
-  s = f2_add(s, exp32<kExact>(rb, kExact ? bits32(lo - 96, hi - 96) : 0u, c2, nm2, pk[3]));
+  uint32_t r[4][32];
+  tmem_ld32_issue(sbuf, r[0]);
+  tmem_ld32_issue(sbuf + 32, r[1]);
+  tmem_wait32(r[0]);
+  tmem_wait32(r[1]);
+  tmem_ld32_issue(sbuf + 64, r[2]);
+  tmem_ld32_issue(sbuf + 96, r[3]);
+  uint64_t s = exp32<kExact>(r[0], kExact ? bits32(lo, hi) : 0u, c2, nm2, pk[0]);
+  s = f2_add(s, exp32<kExact>(r[1], kExact ? bits32(lo - 32, hi - 32) : 0u, c2, nm2, pk[1]));
+  tmem_wait32(r[2]);
+  tmem_wait32(r[3]);
+  s = f2_add(s, exp32<kExact>(r[2], kExact ? bits32(lo - 64, hi - 64) : 0u, c2, nm2, pk[2]));
+  s = f2_add(s, exp32<kExact>(r[3], kExact ? bits32(lo - 96, hi - 96) : 0u, c2, nm2, pk[3]));
   float s0, s1;
   f2_unpack(s, s0, s1);
   return s0 + s1;
@@ -315,7 +315,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_dense_kernel(
     }
     for (int b = 0; b < 3; ++b) {
       mbar_init(&bars.sfull[b], 1);
-      mbar_init(&bars.pready[b], 128 + 1);                // the group's rows and the tiles
+      mbar_init(&bars.pready[b], 4 + 1);                  // the group's warps and the tile watch
     }
     mbar_init(&bars.done, 1);
     mbar_fence_init();
@@ -448,8 +448,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_dense_kernel(
       // warp's are all in the way.
       for (int t = 0; t < T; ++t) {
         if (!wait_slot(slot_v(t, T)) || (t + 3 < T && !wait_slot(slot_k(t + 3)))) break;
-        // the phase before has to be over, or this would count for it
-        if (t >= 3 && !wait_p(t - 3)) break;
+        // the phase before has to be over, or this would count for it: S(t) is behind PV(t - 3)
+        if (!wait_s(t)) break;
         if (elect_one()) mbar_arrive(&bars.pready[t % 3]);
         __syncwarp();
       }
@@ -557,7 +557,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_dense_kernel(
         fence_proxy_async_smem();
       }
       tc_fence_before_sync();
-      mbar_arrive(&bars.pready[t % 3]);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars.pready[t % 3]);
     }
     // ---- epilogue: each group's warps store half of the columns
     if (ok && T > 0)
