@@ -1020,6 +1020,8 @@ spark_status spark_qk_norm_rope(const void* Q, const void* K, const void* V, int
     a.token_stride[t] = strides ? strides[2 * t + 1] : d;
     if (!in[t]) continue;
     if (!aligned(in[t], esize) || !aligned(out[t], esize)) return SPARK_ERR_INVALID_ARG;
+    for (int u = 0; u < 3; ++u)                  // another tensor's input or output
+      if (u != t && in[u] && (out[t] == in[u] || out[t] == out[u])) return SPARK_ERR_INVALID_ARG;
     // in place: every row is read and written by the same threads, at the same place
     if (in[t] == out[t] && !((H == 1 || a.head_stride[t] == static_cast<long long>(N) * d) &&
                              (N == 1 || a.token_stride[t] == d)))
@@ -1115,6 +1117,8 @@ spark_status spark_attend_dense(const void* Q, const void* K, const void* V, con
   if (!aligned(Q, 16) || !aligned(out, 16) || !aligned(ranges, 16) || !aligned(lse, 4) ||
       (nk > 0 && (!aligned(K, 16) || !aligned(V, 16))) ||
       (nc > 0 && (!aligned(Kc, 16) || !aligned(Vc, 16))))
+    return SPARK_ERR_INVALID_ARG;
+  if (out == Q || (nk > 0 && (out == K || out == V)) || (nc > 0 && (out == Kc || out == Vc)))
     return SPARK_ERR_INVALID_ARG;
   if (!workspace || workspace_bytes < attend_dense_workspace(H, nq, nk, nc, d) ||
       !aligned(workspace, kAlign))

@@ -541,7 +541,8 @@ SPARK_API spark_status spark_bsa_forward_noalloc(const void* Q, const void* K, c
  *     order; inv_freq: device fp32 [pairs].  1 <= naxes <= SPARK_MAX_ROPE_AXES.  With pairs == 0
  *     nothing is rotated and positions, axis_pairs and inv_freq may be NULL.
  *   - Q_out, K_out, V_out: device contiguous [H,N,d] of `dtype`.  An output may be its own input
- *     when that is contiguous [H,N,d]; the tensors must not overlap otherwise. */
+ *     when that is contiguous [H,N,d]; the tensors must not overlap otherwise.  An input may repeat
+ *     itself (strides of 0). */
 #define SPARK_MAX_ROPE_AXES 4
 
 SPARK_API spark_status spark_qk_norm_rope(const void* Q, const void* K, const void* V, int dtype,
@@ -589,10 +590,11 @@ SPARK_API spark_status spark_rope_frequencies(const int32_t* axis_pairs, int nax
  *   - out: [H,nq,d] of out_dtype; lse: fp32 [H,nq], may be NULL.  Neither may overlap an input.
  *   - workspace: device, 256-byte aligned, spark_attend_dense_workspace_size bytes (never 0): the
  *     partial sums of calls with few rows, whose keys are split over the GPU and joined by a
- *     second kernel in a fixed order (results are deterministic).
- *   - Keys of a row's masked places may hold anything, NaN included.  A value row may when no row
- *     of the same 256 consecutive query rows (128 when nq <= 128) has it between the smallest
- *     begin and the largest end of its ranges; elsewhere 0 * NaN reaches the rows that mask it.
+ *     second kernel in a fixed order (results are deterministic).  Calls that may overlap on the
+ *     GPU need a workspace each.
+ *   - Keys of a row's masked places may hold anything, NaN included.  So may a value row that lies
+ *     outside the ranges of its query rows' tile (128 rows from a multiple of 128), from the
+ *     smallest begin to the largest end in it; elsewhere 0 * NaN reaches the rows that mask it.
  *   - bf16 tensor-core products with fp32 sums; probabilities are rounded to bf16. */
 #define SPARK_MAX_DENSE (1 << 30)
 

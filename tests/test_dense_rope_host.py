@@ -15,6 +15,7 @@ from block_sparse_attention_gather_b200 import (
 
 OK, INVALID, UNSUPPORTED, WORKSPACE = 0, 1, 2, 3
 P = ctypes.c_void_p(0x100000)
+OUT = ctypes.c_void_p(0x900000)
 
 
 @pytest.fixture(scope="module")
@@ -26,7 +27,7 @@ def L():
 
 
 def dense(L, **kw):
-    a = dict(Q=P, K=P, V=P, Kc=P, Vc=P, H=2, nq=300, nk=1000, nc=10, d=128, ranges=None, out=P,
+    a = dict(Q=P, K=P, V=P, Kc=P, Vc=P, H=2, nq=300, nk=1000, nc=10, d=128, ranges=None, out=OUT,
              out_dtype=0, lse=P, ws=P, ws_bytes=0, err=None, stream=None)
     a.update(kw)
     return L.spark_attend_dense(*a.values())
@@ -52,6 +53,7 @@ def test_dense_refusals(L):
     assert dense(L, ws=None) == WORKSPACE
     assert dense(L, ws_bytes=100) == WORKSPACE
     assert dense(L, ws=ctypes.c_void_p(0x100010), ws_bytes=1 << 40) == WORKSPACE
+    assert dense(L, out=P, ws_bytes=1 << 40) == INVALID          # over an input
     # an empty key set needs no pointers: the next check is reached
     assert dense(L, K=None, V=None, nk=0) == WORKSPACE
     assert dense(L, Kc=None, Vc=None, nc=0) == WORKSPACE
@@ -81,8 +83,8 @@ def test_ranges_refusals(L):
 def rope(L, **kw):
     a = dict(Q=P, K=P, V=P, dtype=0, H=2, N=10, d=128, strides=None, wq=P, wk=P, eps=1e-6, pos=P,
              f32=0, naxes=1, axis_pairs=(ctypes.c_int32 * 4)(64), pairs=64, freq=P, inter=0,
-             scale=1.0, qo=ctypes.c_void_p(0x900000), ko=ctypes.c_void_p(0x900000),
-             vo=ctypes.c_void_p(0x900000), stream=None)
+             scale=1.0, qo=OUT, ko=ctypes.c_void_p(0xa00000),
+             vo=ctypes.c_void_p(0xb00000), stream=None)
     a.update(kw)
     return L.spark_qk_norm_rope(*a.values())
 
@@ -110,9 +112,11 @@ def test_rope_refusals(L):
     assert rope(L, naxes=5, axis_pairs=(ctypes.c_int32 * 5)(64)) == UNSUPPORTED
     assert rope(L, naxes=2, axis_pairs=(ctypes.c_int32 * 4)(65, -1)) == INVALID
     assert rope(L, Q=ctypes.c_void_p(0x100001)) == INVALID       # half an element
-    # in place needs the output's own layout
+    # in place needs the output's own layout, and no other tensor's place
     strides = (ctypes.c_int64 * 6)(128, 256, 1280, 128, 1280, 128)
-    assert rope(L, qo=P, strides=strides) == INVALID
+    assert rope(L, qo=P, strides=strides, K=None, wk=None, V=None) == INVALID
+    assert rope(L, ko=OUT) == INVALID
+    assert rope(L, qo=ctypes.c_void_p(0x200000), K=ctypes.c_void_p(0x200000)) == INVALID
 
 
 def test_frequencies():

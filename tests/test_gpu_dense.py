@@ -10,6 +10,9 @@ log-sum-exp to 2^-12.
 """
 
 import math
+import os
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -244,6 +247,44 @@ def test_on_another_stream_and_in_graphs_that_share_a_workspace(nq):
     torch.cuda.synchronize()
     for (o, l), w in zip(outs, want):
         assert torch.equal(o, w[0]) and torch.equal(l, w[1])
+
+
+FIRST_CALL = """
+import torch
+from block_sparse_attention_gather_b200 import spark_attend_dense
+Q, K, V = (torch.randn(2, n, 128, device="cuda").bfloat16() for n in (3, 9000, 9000))
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    out, lse = spark_attend_dense(Q, K, V)
+graph.replay()
+want, _ = spark_attend_dense(Q, K, V)
+torch.cuda.synchronize()
+assert torch.equal(out, want)
+"""
+
+
+def test_first_call_of_a_process_may_be_captured():
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    run = subprocess.run([sys.executable, "-c", FIRST_CALL], cwd=root, capture_output=True,
+                         text=True, timeout=120)
+    assert run.returncode == 0, run.stderr[-2000:]
+
+
+def test_two_streams_at_once():
+    """Calls that overlap on the GPU, each with a workspace of its own."""
+    xs = [inputs(40 + i, 2, 9 + 200 * i, 20000, 50, 128) for i in range(2)]
+    want = [spark_attend_dense(**x) for x in xs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in xs]
+    got = [[], []]
+    for _ in range(5):
+        for i, (x, s) in enumerate(zip(xs, streams)):
+            with torch.cuda.stream(s):
+                got[i].append(spark_attend_dense(**x))
+    torch.cuda.synchronize()
+    for g, w in zip(got, want):
+        assert all(torch.equal(o, w[0]) and torch.equal(l, w[1]) for o, l in g)
 
 
 @pytest.mark.parametrize("nq", [5, 300])

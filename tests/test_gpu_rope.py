@@ -134,6 +134,21 @@ def test_in_place_and_on_another_stream(interleaved):
         assert torch.equal(a, b)
 
 
+def test_inputs_that_repeat_themselves():
+    """Strides of 0: one head shared by all (Q), one token by all (K)."""
+    H, N, d = 5, 60, 128
+    one = torch.randn(1, N, d, device=DEV).to(BF)
+    row = torch.randn(H, 1, d, device=DEV).to(BF)
+    w = torch.rand(d, device=DEV) + 0.5
+    pos = torch.arange(N, device=DEV, dtype=torch.int32)[:, None]
+    freq = spark_rope_frequencies([64])[0].to(DEV)
+    q, k, v = spark_qk_norm_rope(one.expand(H, N, d), row.expand(H, N, d), one.expand(H, N, d), w, w,
+                                 1e-6, pos, freq, [64], True)
+    check(q, reference(one.expand(H, N, d), w, 1e-6, pos, freq, [64], True, 1.0))
+    check(k, reference(row.expand(H, N, d), w, 1e-6, pos, freq, [64], True, 1.0))
+    assert torch.equal(v, one.expand(H, N, d))
+
+
 def test_zero_rows_infinities_and_graph_replay():
     (Q, K, V), g = inputs(6, 2, 20, 128, torch.float32, packed=False)
     Q[0, 3] = 0
