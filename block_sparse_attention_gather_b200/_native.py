@@ -7,7 +7,6 @@ There is no fallback: if the library is missing or was built for another GPU the
 
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 
@@ -877,11 +876,15 @@ def spark_bsa_forward_host(Q, K, V, q_perm, k_perm, q_offsets, k_offsets, topk_r
 
 # ------------------------------------------------ norm and rotation, dense attention
 
-def _on(index):
-    """Makes device `index` current for a launch on one of its streams (a no-op when it is)."""
+# The calls below can take as long on the host as their kernels do on the GPU, so the usual case of
+# a check is one expression, and the messages are made where one fails.
+
+def _launch(index, fn, *args):
+    """fn(*args) with device `index` current, whose stream the arguments name."""
     if index == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    return torch.cuda.device(index)
+        return fn(*args)
+    with torch.cuda.device(index):
+        return fn(*args)
 
 
 def _stream_of(index, stream):
@@ -890,13 +893,17 @@ def _stream_of(index, stream):
     return stream.cuda_stream
 
 
-def _check_one(t, name, dtype, device, index):
-    """_need for one dtype, the usual case in one expression: these calls can take as long on the
-    host as their kernels do on the GPU.  Returns the address."""
-    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == index
-            and t.is_contiguous()):
-        _need(t, name, dtype, device)
-    return t.data_ptr()
+def _refuse(t, name, dtype, device, shape):
+    """Raises what is wrong with a tensor that failed its check."""
+    _need(t, name, dtype, device)
+    raise ValueError(f"{name} must have the shape {shape}")
+
+
+def _type_error(required, **tensors):
+    """An attribute was missing: names the argument that is no tensor."""
+    for name, t in tensors.items():
+        if not isinstance(t, torch.Tensor) and (t is not None or name in required):
+            raise TypeError(f"{name} must be a torch.Tensor") from None
 
 
 def spark_rope_frequencies(axis_pairs, base=10000.0, scaling="none", factor=1.0, original=0.0):
@@ -913,21 +920,26 @@ def spark_rope_frequencies(axis_pairs, base=10000.0, scaling="none", factor=1.0,
     return out[:sum(int(p) for p in axis_pairs)], scale.value
 
 
-def _check_rows(t, name, dtype, shape, device, index):
-    """_check_one for a tensor [H, N, d] whose last dimension alone has to be contiguous."""
-    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == index
-            and t.dim() == 3):
-        _need(t.contiguous() if isinstance(t, torch.Tensor) else t, name, dtype, device)
-        raise ValueError(f"{name} must have the shape [H, N, d]")
-    if shape is not None and t.shape != shape:
-        raise ValueError(f"{name} must have the shape [H, N, d] of Q")
-    head, token, inner = t.stride()
-    if inner != 1:
+def _refuse_rows(t, name, dtype, device):
+    """_refuse for a tensor [H, N, d] whose last dimension alone has to be contiguous."""
+    if t.dim() == 3 and t.stride(2) != 1:
         raise ValueError(f"{name}: the last dimension must be contiguous")
-    return t.data_ptr(), head, token
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    _refuse(t.contiguous(), name, dtype, device, "[H, N, d] of Q")
 
 
 _Strides = ctypes.c_int64 * 6
+_AXES = {}                       # axis counts -> (their sum, the array the library takes)
+
+
+def _axes(axis_pairs):
+    key = tuple(axis_pairs)
+    if key not in _AXES:
+        if len(_AXES) > 256:
+            _AXES.clear()
+        _AXES[key] = (sum(key), (ctypes.c_int32 * len(key))(*key))
+    return _AXES[key]
 
 
 def spark_qk_norm_rope(Q, K=None, V=None, q_weight=None, k_weight=None, eps=1e-6, positions=None,
@@ -938,64 +950,91 @@ def spark_qk_norm_rope(Q, K=None, V=None, q_weight=None, k_weight=None, eps=1e-6
     out along.  Weights fp32 [d] (None: no norm); positions [N, axes] int32 or fp32; inv_freq
     fp32 [pairs], axis_pairs the pairs of each axis (None: one axis).  Returns (Q_out, K_out,
     V_out), None for what is absent."""
-    if not (isinstance(Q, torch.Tensor) and Q.is_cuda):
-        _need(Q, "Q")
-    dev, dt, shape = Q.device, Q.dtype, Q.shape
-    code, index = _code(dt), dev.index
-    q, qh, qt = _check_rows(Q, "Q", dt, None, dev, index)
-    H, N, d = shape
-    k = v = kh = kt = vh = vt = 0
-    if K is not None:
-        k, kh, kt = _check_rows(K, "K", dt, shape, dev, index)
-    elif K_out is not None or k_weight is not None:
-        raise ValueError("K_out and k_weight need K")
-    if V is not None:
-        v, vh, vt = _check_rows(V, "V", dt, shape, dev, index)
-    elif V_out is not None:
-        raise ValueError("V_out needs V")
-    outs = [Q_out, K_out, V_out]
-    ptrs = [None, None, None]
-    for i, x in enumerate((q, k, v)):
-        if x == 0 and i:
-            continue
-        if outs[i] is None:
-            outs[i] = torch.empty(shape, dtype=dt, device=dev)
-        elif outs[i].shape != shape:
-            raise ValueError(f"{'QKV'[i]}_out must have the shape [H, N, d] of Q")
-        ptrs[i] = _check_one(outs[i], "QKV"[i] + "_out", dt, dev, index)
     f32 = torch.float32
-    wq = wk = None
-    if q_weight is not None:
-        wq = _check_one(q_weight, "q_weight", f32, dev, index)
-        if q_weight.numel() != d:
-            raise ValueError("q_weight must have the shape [d]")
-    if k_weight is not None:
-        wk = _check_one(k_weight, "k_weight", f32, dev, index)
-        if k_weight.numel() != d:
-            raise ValueError("k_weight must have the shape [d]")
-    pairs, naxes, counts, pos, freq, pos_f32 = 0, 0, None, None, None, False
-    if inv_freq is not None:
-        freq = _check_one(inv_freq, "inv_freq", f32, dev, index)
-        if positions is None:
-            raise ValueError("inv_freq needs positions")
-        pos_f32 = positions.dtype is f32
-        pos = _check_one(positions, "positions", f32 if pos_f32 else torch.int32, dev, index)
-        pairs, naxes = inv_freq.numel(), 1 if positions.dim() == 1 else positions.shape[-1]
-        if positions.dim() not in (1, 2) or positions.shape[0] != N:
-            raise ValueError("positions must have the shape [N, axes]")
-        axis_pairs = (pairs,) if axis_pairs is None else axis_pairs
-        if len(axis_pairs) != naxes or sum(axis_pairs) != pairs:
-            raise ValueError("axis_pairs must give every axis of positions its pairs of inv_freq")
-        counts = (ctypes.c_int32 * naxes)(*axis_pairs)
-    elif positions is not None or axis_pairs is not None:
-        raise ValueError("positions and axis_pairs need inv_freq")
-    with _on(index):
-        st = lib().spark_qk_norm_rope(q, k or None, v or None, code, H, N, d,
-                                      _Strides(qh, qt, kh, kt, vh, vt), wq, wk, eps, pos, pos_f32,
-                                      naxes, counts, pairs, freq, bool(interleaved), rope_scale,
-                                      *ptrs, _stream_of(index, stream))
-    _check("spark_qk_norm_rope", st)
-    return tuple(outs)
+    try:
+        index, dt, shape = Q.get_device(), Q.dtype, Q.shape
+        if index < 0 or len(shape) != 3:
+            _refuse(Q.contiguous(), "Q", (torch.bfloat16, f32), None, "[H, N, d]")
+        code = _code(dt)
+        H, N, d = shape
+        q, (qh, qt, inner) = Q.data_ptr(), Q.stride()
+        if inner != 1:
+            _refuse_rows(Q, "Q", dt, Q.device)
+        if Q_out is None:
+            Q_out = torch.empty(shape, dtype=dt, device=Q.device)
+        if not (Q_out.dtype is dt and Q_out.get_device() == index and Q_out.is_contiguous()
+                and Q_out.shape == shape):
+            _refuse(Q_out, "Q_out", dt, Q.device, "[H, N, d] of Q")
+        k = v = ko = vo = None
+        kh = kt = vh = vt = 0
+        if K is not None:
+            k, (kh, kt, inner) = K.data_ptr(), K.stride()
+            if inner != 1 or not (K.dtype is dt and K.get_device() == index and K.shape == shape):
+                _refuse_rows(K, "K", dt, Q.device)
+            if K_out is None:
+                K_out = torch.empty(shape, dtype=dt, device=Q.device)
+            if not (K_out.dtype is dt and K_out.get_device() == index and K_out.is_contiguous()
+                    and K_out.shape == shape):
+                _refuse(K_out, "K_out", dt, Q.device, "[H, N, d] of Q")
+            ko = K_out.data_ptr()
+        elif K_out is not None or k_weight is not None:
+            raise ValueError("K_out and k_weight need K")
+        if V is not None:
+            v, (vh, vt, inner) = V.data_ptr(), V.stride()
+            if inner != 1 or not (V.dtype is dt and V.get_device() == index and V.shape == shape):
+                _refuse_rows(V, "V", dt, Q.device)
+            if V_out is None:
+                V_out = torch.empty(shape, dtype=dt, device=Q.device)
+            if not (V_out.dtype is dt and V_out.get_device() == index and V_out.is_contiguous()
+                    and V_out.shape == shape):
+                _refuse(V_out, "V_out", dt, Q.device, "[H, N, d] of Q")
+            vo = V_out.data_ptr()
+        elif V_out is not None:
+            raise ValueError("V_out needs V")
+        wq = wk = None
+        if q_weight is not None:
+            if not (q_weight.dtype is f32 and q_weight.get_device() == index
+                    and q_weight.is_contiguous() and q_weight.numel() == d):
+                _refuse(q_weight, "q_weight", f32, Q.device, "[d]")
+            wq = q_weight.data_ptr()
+        if k_weight is not None:
+            if not (k_weight.dtype is f32 and k_weight.get_device() == index
+                    and k_weight.is_contiguous() and k_weight.numel() == d):
+                _refuse(k_weight, "k_weight", f32, Q.device, "[d]")
+            wk = k_weight.data_ptr()
+        pairs, naxes, counts, pos, freq, pos_f32 = 0, 0, None, None, None, False
+        if inv_freq is not None:
+            if positions is None:
+                raise ValueError("inv_freq needs positions")
+            pairs = inv_freq.numel()
+            if not (inv_freq.dtype is f32 and inv_freq.get_device() == index
+                    and inv_freq.is_contiguous()):
+                _refuse(inv_freq, "inv_freq", f32, Q.device, "[pairs]")
+            pos_f32 = positions.dtype is f32
+            size = positions.shape
+            naxes = size[1] if len(size) == 2 else 1
+            if not ((pos_f32 or positions.dtype is torch.int32)
+                    and positions.get_device() == index and positions.is_contiguous()
+                    and 1 <= len(size) <= 2 and size[0] == N):
+                _refuse(positions, "positions", (torch.int32, f32), Q.device, "[N, axes]")
+            total, counts = _axes((pairs,) if axis_pairs is None else axis_pairs)
+            if total != pairs or len(counts) != naxes:
+                raise ValueError("axis_pairs must give every axis of positions its pairs of "
+                                 "inv_freq")
+            pos, freq = positions.data_ptr(), inv_freq.data_ptr()
+        elif positions is not None or axis_pairs is not None:
+            raise ValueError("positions and axis_pairs need inv_freq")
+    except AttributeError:
+        _type_error(("Q",), Q=Q, K=K, V=V, q_weight=q_weight, k_weight=k_weight, positions=positions,
+                    inv_freq=inv_freq, Q_out=Q_out, K_out=K_out, V_out=V_out)
+        raise
+    st = _launch(index, lib().spark_qk_norm_rope, q, k, v, code, H, N, d,
+                 _Strides(qh, qt, kh, kt, vh, vt), wq, wk, eps, pos, pos_f32, naxes, counts, pairs,
+                 freq, bool(interleaved), rope_scale, Q_out.data_ptr(), ko, vo,
+                 _stream_of(index, stream))
+    if st:
+        _check("spark_qk_norm_rope", st)
+    return Q_out, K_out, V_out
 
 
 def spark_attend_ranges(nq, q_offsets, k_offsets=None, c_offsets=None, prefix=None, causal=False,
@@ -1005,29 +1044,41 @@ def spark_attend_ranges(nq, q_offsets, k_offsets=None, c_offsets=None, prefix=No
     own place or the segment's prefix."""
     i32 = torch.int32
     _need(q_offsets, "q_offsets", i32)
-    dev, n = q_offsets.device, q_offsets.numel()
-    index = dev.index
-    ptrs = []
-    for name, t, size in (("k_offsets", k_offsets, n), ("c_offsets", c_offsets, n),
-                          ("prefix", prefix, n - 1)):
-        if t is None:
-            ptrs.append(None)
-            continue
-        ptrs.append(_check_one(t, name, i32, dev, index))
-        if t.numel() != size:
-            raise ValueError(f"{name} must hold {size} values")
-    if prefix is not None and not causal:
-        raise ValueError("prefix needs causal")
-    if ranges is None:
-        ranges = torch.empty(max(int(nq), 0), 4, dtype=i32, device=dev)
-    out = _check_one(ranges, "ranges", i32, dev, index)
-    if ranges.shape != (nq, 4):
-        raise ValueError("ranges must have the shape [nq, 4]")
-    flags = None if err is None else _check_one(err, "err", i32, dev, index)
-    with _on(index):
-        st = lib().spark_attend_ranges(nq, n - 1, q_offsets.data_ptr(), *ptrs, bool(causal), out,
-                                       flags, _stream_of(index, stream))
-    _check("spark_attend_ranges", st)
+    index, n = q_offsets.get_device(), q_offsets.numel()
+    try:
+        k = c = p = e = None
+        if k_offsets is not None:
+            if not (k_offsets.dtype is i32 and k_offsets.get_device() == index
+                    and k_offsets.is_contiguous() and k_offsets.numel() == n):
+                _refuse(k_offsets, "k_offsets", i32, q_offsets.device, f"[{n}]")
+            k = k_offsets.data_ptr()
+        if c_offsets is not None:
+            if not (c_offsets.dtype is i32 and c_offsets.get_device() == index
+                    and c_offsets.is_contiguous() and c_offsets.numel() == n):
+                _refuse(c_offsets, "c_offsets", i32, q_offsets.device, f"[{n}]")
+            c = c_offsets.data_ptr()
+        if prefix is not None:
+            if not causal:
+                raise ValueError("prefix needs causal")
+            if not (prefix.dtype is i32 and prefix.get_device() == index
+                    and prefix.is_contiguous() and prefix.numel() == n - 1):
+                _refuse(prefix, "prefix", i32, q_offsets.device, f"[{n - 1}]")
+            p = prefix.data_ptr()
+        if ranges is None:
+            ranges = torch.empty(max(int(nq), 0), 4, dtype=i32, device=q_offsets.device)
+        if not (ranges.dtype is i32 and ranges.get_device() == index and ranges.is_contiguous()
+                and ranges.shape == (nq, 4)):
+            _refuse(ranges, "ranges", i32, q_offsets.device, "[nq, 4]")
+        if err is not None:
+            _need(err, "err", i32, q_offsets.device)
+            e = err.data_ptr()
+    except AttributeError:
+        _type_error((), k_offsets=k_offsets, c_offsets=c_offsets, prefix=prefix, ranges=ranges)
+        raise
+    st = _launch(index, lib().spark_attend_ranges, nq, n - 1, q_offsets.data_ptr(), k, c, p,
+                 bool(causal), ranges.data_ptr(), e, _stream_of(index, stream))
+    if st:
+        _check("spark_attend_ranges", st)
     return ranges
 
 
@@ -1040,46 +1091,66 @@ def spark_attend_dense(Q, K, V, Kc=None, Vc=None, ranges=None, out_dtype=torch.b
     """Dense attention of the rows of Q [H, nq, d] over the video keys K, V [H, nk, d] and the
     context keys Kc, Vc [H, nc, d] (bf16), each row over its ranges ([nq, 4] int32, None: all);
     returns (out, lse)."""
-    bf, i32 = torch.bfloat16, torch.int32
-    _need(Q, "Q", bf)
-    dev = Q.device
-    index = dev.index
-    if Q.dim() != 3:
-        raise ValueError("Q must have the shape [H, nq, d]")
-    H, nq, d = shape = Q.shape
-    k, v = _check_one(K, "K", bf, dev, index), _check_one(V, "V", bf, dev, index)
-    if K.dim() != 3 or K.shape[0] != H or K.shape[2] != d or V.shape != K.shape:
-        raise ValueError("K and V must have the shape [H, nk, d]")
-    nk, nc, kc, vc = K.shape[1], 0, None, None
-    if Kc is not None or Vc is not None:
-        kc, vc = _check_one(Kc, "Kc", bf, dev, index), _check_one(Vc, "Vc", bf, dev, index)
-        if Kc.dim() != 3 or Kc.shape[0] != H or Kc.shape[2] != d or Vc.shape != Kc.shape:
-            raise ValueError("Kc and Vc must have the shape [H, nc, d]")
-        nc = Kc.shape[1]
-    rg = None
-    if ranges is not None:
-        rg = _check_one(ranges, "ranges", i32, dev, index)
-        if ranges.shape != (nq, 4):
-            raise ValueError("ranges must have the shape [nq, 4]")
-    if out is None:
-        out = torch.empty(shape, dtype=out_dtype, device=dev)
-    code = _code(out.dtype)
-    o = _check_one(out, "out", out.dtype, dev, index)
-    if lse is None:
-        lse = torch.empty(H, nq, dtype=torch.float32, device=dev)
-    m = _check_one(lse, "lse", torch.float32, dev, index)
-    if out.shape != shape or lse.shape != (H, nq):
-        raise ValueError("out and lse must have the shapes [H, nq, d] and [H, nq]")
-    if workspace is None:
-        workspace = torch.empty(spark_attend_dense_workspace_size(H, nq, nk, nc, d),
-                                dtype=torch.uint8, device=dev)
-    ws = _check_one(workspace, "workspace", torch.uint8, dev, index)
-    flags = None if err is None else _check_one(err, "err", i32, dev, index)
-    with _on(index):
-        st = lib().spark_attend_dense(Q.data_ptr(), k, v, kc, vc, H, nq, nk, nc, d, rg,
-                                      o, code, m, ws, workspace.numel(), flags,
-                                      _stream_of(index, stream))
-    _check("spark_attend_dense", st)
+    bf, i32, f32 = torch.bfloat16, torch.int32, torch.float32
+    try:
+        index, shape = Q.get_device(), Q.shape
+        if not (Q.dtype is bf and index >= 0 and Q.is_contiguous() and len(shape) == 3):
+            _refuse(Q, "Q", bf, None, "[H, nq, d]")
+        H, nq, d = shape
+        if not (K.dtype is bf and K.get_device() == index and K.is_contiguous() and K.dim() == 3):
+            _refuse(K, "K", bf, Q.device, "[H, nk, d]")
+        keys = K.shape
+        nk, nc, kc, vc, rg, e = keys[1], 0, None, None, None, None
+        if keys[0] != H or keys[2] != d:
+            raise ValueError("K and V must have the shape [H, nk, d]")
+        if not (V.dtype is bf and V.get_device() == index and V.is_contiguous()
+                and V.shape == keys):
+            _refuse(V, "V", bf, Q.device, "[H, nk, d]")
+        if Kc is not None or Vc is not None:
+            if not (Kc.dtype is bf and Kc.get_device() == index and Kc.is_contiguous()
+                    and Kc.dim() == 3):
+                _refuse(Kc, "Kc", bf, Q.device, "[H, nc, d]")
+            keys = Kc.shape
+            if keys[0] != H or keys[2] != d:
+                raise ValueError("Kc and Vc must have the shape [H, nc, d]")
+            if not (Vc.dtype is bf and Vc.get_device() == index and Vc.is_contiguous()
+                    and Vc.shape == keys):
+                _refuse(Vc, "Vc", bf, Q.device, "[H, nc, d]")
+            nc, kc, vc = keys[1], Kc.data_ptr(), Vc.data_ptr()
+        if ranges is not None:
+            if not (ranges.dtype is i32 and ranges.get_device() == index
+                    and ranges.is_contiguous() and ranges.shape == (nq, 4)):
+                _refuse(ranges, "ranges", i32, Q.device, "[nq, 4]")
+            rg = ranges.data_ptr()
+        if out is None:
+            out = torch.empty(shape, dtype=out_dtype, device=Q.device)
+        code = _code(out.dtype)
+        if not (out.get_device() == index and out.is_contiguous() and out.shape == shape):
+            _refuse(out, "out", out.dtype, Q.device, "[H, nq, d] of Q")
+        if lse is None:
+            lse = torch.empty(H, nq, dtype=f32, device=Q.device)
+        if not (lse.dtype is f32 and lse.get_device() == index and lse.is_contiguous()
+                and lse.shape == (H, nq)):
+            _refuse(lse, "lse", f32, Q.device, "[H, nq]")
+        if workspace is None:
+            workspace = torch.empty(spark_attend_dense_workspace_size(H, nq, nk, nc, d),
+                                    dtype=torch.uint8, device=Q.device)
+        if not (workspace.dtype is torch.uint8 and workspace.get_device() == index
+                and workspace.is_contiguous()):
+            _need(workspace, "workspace", torch.uint8, Q.device)
+        if err is not None:
+            _need(err, "err", i32, Q.device)
+            e = err.data_ptr()
+    except AttributeError:
+        both = () if Kc is None and Vc is None else ("Kc", "Vc")
+        _type_error(("Q", "K", "V", *both), Q=Q, K=K, V=V, Kc=Kc, Vc=Vc, ranges=ranges, out=out,
+                    lse=lse, workspace=workspace)
+        raise
+    st = _launch(index, lib().spark_attend_dense, Q.data_ptr(), K.data_ptr(), V.data_ptr(), kc, vc,
+                 H, nq, nk, nc, d, rg, out.data_ptr(), code, lse.data_ptr(), workspace.data_ptr(),
+                 workspace.numel(), e, _stream_of(index, stream))
+    if st:
+        _check("spark_attend_dense", st)
     return out, lse
 
 
@@ -1122,11 +1193,9 @@ def spark_bsa_forward_joint(Q, K, V, Qc, Kc, Vc, q_perm, k_perm, q_offsets, k_of
         size = spark_bsa_workspace_size_joint(H, N, d, nqb, nkb, topk_ratio, nc)
         workspace = torch.empty(size, dtype=torch.uint8, device=dev)
     _need(workspace, "workspace", torch.uint8, dev)
-    with _on(dev.index):
-        st = lib().spark_bsa_forward_joint(
-            _ptr(Q), _ptr(K), _ptr(V), _ptr(Qc), _ptr(Kc), _ptr(Vc), nc, _code(Q.dtype), H, N, d,
-            _ptr(q_perm), _ptr(k_perm), _ptr(q_offsets), nqb, _ptr(k_offsets), nkb,
-            float(topk_ratio), _ptr(out), _ptr(out_c), _ptr(workspace), workspace.numel(),
-            _stream_of(dev.index, stream))
+    st = _launch(dev.index, lib().spark_bsa_forward_joint, _ptr(Q), _ptr(K), _ptr(V), _ptr(Qc),
+                 _ptr(Kc), _ptr(Vc), nc, _code(Q.dtype), H, N, d, _ptr(q_perm), _ptr(k_perm),
+                 _ptr(q_offsets), nqb, _ptr(k_offsets), nkb, float(topk_ratio), _ptr(out),
+                 _ptr(out_c), _ptr(workspace), workspace.numel(), _stream_of(dev.index, stream))
     _check("spark_bsa_forward_joint", st)
     return out, out_c, workspace, layout

@@ -201,8 +201,10 @@ def test_binding_refuses_host_tensors_and_types():
         spark_attend_dense(t, t, t)
     with pytest.raises(ValueError, match="CUDA tensor"):
         spark_qk_norm_rope(t, t, t)
-    with pytest.raises(TypeError):
+    with pytest.raises(TypeError, match="Q must be"):
         spark_qk_norm_rope([1, 2], t)
+    with pytest.raises(TypeError, match="Q must be"):
+        spark_attend_dense(None or [1], t, t)
     with pytest.raises(ValueError, match="CUDA tensor"):
         spark_attend_ranges(4, torch.zeros(2, dtype=torch.int32))
     perm = torch.zeros(1, 8, dtype=torch.int32)

@@ -426,3 +426,29 @@ def test_projection_to_joint_attention():
     P.compare_out(P.to64(out), P.to64(dense), "video rows at ratio 1")
     ref, _, A = reference(dict(Q=Qc, K=K, V=V, Kc=Kc, Vc=Vc))
     assert ((out_c.double() - ref).abs() <= (2.0 ** -8 + 2.0 ** -12) * A + 2.0 ** -8 * ref.abs()).all()
+
+
+def test_binding_refusals():
+    x = inputs(50, 2, 5, 40, 7, 64)
+    r = torch.zeros(5, 4, dtype=torch.int32, device=DEV)
+    good = dict(x, ranges=r)
+    spark_attend_dense(**good)
+    for name, bad, kind in (
+            ("Q", x["Q"].float(), TypeError), ("Q", x["Q"][:, ::2], ValueError),
+            ("Q", x["Q"][0], ValueError), ("K", x["K"].cpu(), ValueError),
+            ("K", x["K"][:1], ValueError), ("V", x["V"][:, :9].contiguous(), ValueError),
+            ("V", None, TypeError), ("Kc", x["Kc"].half(), TypeError), ("Vc", None, TypeError),
+            ("Vc", x["Vc"][:, :3].contiguous(), ValueError), ("ranges", r.long(), TypeError),
+            ("ranges", r[:4], ValueError), ("out", x["Q"].half(), TypeError),
+            ("out", x["Q"][:1].contiguous(), ValueError), ("lse", r, TypeError),
+            ("lse", torch.zeros(2, 4, device=DEV), ValueError), ("workspace", r, TypeError),
+            ("err", torch.zeros(1, device=DEV), TypeError)):
+        with pytest.raises((kind,) if kind is not TypeError else (TypeError, ValueError)):
+            spark_attend_dense(**{**good, name: bad})
+    q = torch.tensor([0, 3, 5], dtype=torch.int32, device=DEV)
+    for args, kw in (((5, q.long()), {}), ((5, q, q[:2]), {}), ((5, q, q.cpu()), {}),
+                     ((5, q, None, q), dict(prefix=q, causal=True)),
+                     ((5, q, None, q), dict(prefix=q[:2])), ((5, q), dict(ranges=r[:4])),
+                     ((5, q, [1, 2, 3]), {})):
+        with pytest.raises((TypeError, ValueError)):
+            spark_attend_ranges(*args, **kw)

@@ -12,7 +12,8 @@ import math
 import pytest
 import torch
 
-from block_sparse_attention_gather_b200 import spark_qk_norm_rope, spark_rope_frequencies
+from block_sparse_attention_gather_b200 import (SparkError, spark_qk_norm_rope,
+                                                spark_rope_frequencies)
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -178,3 +179,24 @@ def test_more_elements_than_32_bits():
     freq = spark_rope_frequencies([64])[0].to(DEV)
     spark_qk_norm_rope(Q, q_weight=w, positions=pos, inv_freq=freq, Q_out=Q)
     check(Q[:, -50:], reference(last, w, 1e-6, pos[-50:], freq, [64], False, 1.0))
+
+
+def test_binding_refusals():
+    (Q, K, V), g = inputs(9, 2, 6, 64, BF, packed=False)
+    w = torch.ones(64, device=DEV)
+    pos = torch.zeros(6, 2, dtype=torch.int32, device=DEV)
+    f = torch.ones(10, device=DEV)
+    good = dict(Q=Q, K=K, V=V, q_weight=w, k_weight=w, positions=pos, inv_freq=f, axis_pairs=[4, 6])
+    spark_qk_norm_rope(**good)
+    for change in (dict(Q=Q.half()), dict(Q=Q[0]), dict(Q=Q.cpu()), dict(Q=Q.transpose(1, 2)),
+                   dict(K=K.float()), dict(K=K[:1]), dict(K=None), dict(V=V[:, :3]), dict(V=[1]),
+                   dict(q_weight=w.to(BF)), dict(k_weight=w[:32]), dict(positions=pos.long()),
+                   dict(positions=pos[:5]), dict(positions=None), dict(inv_freq=None),
+                   dict(inv_freq=f.double()), dict(axis_pairs=[4, 5]), dict(axis_pairs=[10]),
+                   dict(axis_pairs=None), dict(Q_out=Q.float()), dict(K_out=K[:, :5].contiguous()),
+                   dict(Q_out=V.transpose(0, 1))):
+        with pytest.raises((TypeError, ValueError)):
+            spark_qk_norm_rope(**{**good, **change})
+    for change in (dict(axis_pairs=[-1, 11]), dict(eps=-1.0), dict(Q_out=K), dict(V_out=Q)):
+        with pytest.raises(SparkError):
+            spark_qk_norm_rope(**{**good, **change})
