@@ -1025,8 +1025,8 @@ def spark_qk_norm_rope(Q, K=None, V=None, q_weight=None, k_weight=None, eps=1e-6
         elif positions is not None or axis_pairs is not None:
             raise ValueError("positions and axis_pairs need inv_freq")
     except AttributeError:
-        _type_error(("Q",), Q=Q, K=K, V=V, q_weight=q_weight, k_weight=k_weight, positions=positions,
-                    inv_freq=inv_freq, Q_out=Q_out, K_out=K_out, V_out=V_out)
+        _type_error(("Q",), Q=Q, K=K, V=V, q_weight=q_weight, k_weight=k_weight,
+                    positions=positions, inv_freq=inv_freq, Q_out=Q_out, K_out=K_out, V_out=V_out)
         raise
     st = _launch(index, lib().spark_qk_norm_rope, q, k, v, code, H, N, d,
                  _Strides(qh, qt, kh, kt, vh, vt), wq, wk, eps, pos, pos_f32, naxes, counts, pairs,

@@ -8,11 +8,11 @@
 //
 // One pass over the keys with a running reference per row (an online softmax):
 //   p_j = 2^(s_j log2e - ref),  l = sum p,  O = sum p v,  out = O / l,  lse = (ref + log2 l) ln2.
-// ref is the row's maximum over the first two tiles (the first with a live key).  It is raised to a later tile's
-// maximum, and O and l rescaled, only when that tile's sum of p reaches 2^24 (or is no number):
-// up to there p, rounded to bf16 for the tensor cores, and the fp32 sums keep their relative
-// accuracy, so a reference below the true maximum costs none, and the usual tile needs no
-// maximum at all.  The scores stay in TMEM until the sum is known, so the tile can be redone.
+// ref is the row's maximum over the first two tiles (the first with a live key).  It is raised to
+// a later tile's maximum, and O and l rescaled, only when that tile's sum of p reaches 2^24 (or is
+// no number): up to there p, rounded to bf16 for the tensor cores, and the fp32 sums keep their
+// relative accuracy, so a reference below the true maximum costs none, and the usual tile needs
+// no maximum at all.  The scores stay in TMEM until the sum is known, so the tile can be redone.
 //
 // One CTA works on one head, one 128-row query tile and one slice of the key tiles.  12 warps:
 // 0-3 / 4-7 the softmax groups, which take the even and the odd key tiles (warp w owns TMEM lanes
@@ -27,6 +27,23 @@
 // Keys beyond a row's ranges are masked to -inf by value, so what they hold (NaN included) does
 // not matter; rows of V outside the ranges of the whole query tile are zeroed in shared memory
 // before the product, as 0 * NaN would not be 0.
+//
+// What bounds it.  Few rows: reading K and V once (24 heads x 60480 keys, one row: 127 us =
+// 5.9 TB/s); the keys are split over the SMs and joined.  Many rows: the exponentials, with the
+// tensor pipe at 63% of its cycles next to them.  Two softmax warps share a scheduler and take
+// about 1700 cycles a tile each, of which 700 are the special-function unit's (88 of the 128
+// exponentials of a row's tile; the others by polynomial) and the rest the latencies of some 700
+// instructions in order; the MMAs of a tile take 1024 cycles, and reading Q, K, V and writing K, V
+// in shared memory 1280.  24 heads x 30240 x 30240 take 9.05 ms alone (1241 TFLOP/s) and 10.0 ms
+// in a loop at the 1000 W power cap (1120 TFLOP/s at 1470 MHz).
+//
+// The steps, on that case unless named: running maximum, pair of query tiles per CTA 10.9 ms;
+// no maximum per tile 10.3; registers moved to the softmax warps, polynomial 9.7; tile waits in a
+// warp of their own 9.3 (a barrier test takes a few hundred cycles while the MMAs read shared
+// memory); one query tile per CTA, three S buffers, common reference 9.5 against 10.6 on one box,
+// and packed prompts 58 -> 40 us; late query tiles first 285 -> 272 us (8191 causal rows).
+// Measured and not kept: S in 64-key units (an M = 128 MMA takes 64 cycles for N = 64 too), P
+// handed over in halves, CTA pairs with M = 256 (no faster: the exponentials bound both).
 //
 // Every wait is bounded (see spark_ptx.cuh); on expiry the kernel flags kErrTimeout, drains its
 // copies and MMAs, frees TMEM and returns.
@@ -51,7 +68,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kMaxSum = 0x1p24f;           // a tile's sum of p from which the reference is raised
 constexpr int kMaxSplits = 64;
-constexpr int kPolyEvery = 3;                // of 16 pairs of exponentials every third by polynomial
+constexpr int kPolyEvery = 3;                // every third pair of exponentials by polynomial
 
 template <int D>
 struct Cfg {
@@ -630,8 +647,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_dense_kernel(
 
 // Joins the slices of a row: out = sum_s 2^(ref_s - ref) O_s / sum_s 2^(ref_s - ref) l_s with
 // ref the largest, in the order of the slices.  One warp per row, D/32 columns per lane; the
-// slices' references come a lane each (up to 64), and eight slices' columns are loaded at once:
-// one at a time, the loads' latency took 10 us for 16 slices.
+// slices' references come a lane each (up to 64), and eight slices' columns are loaded at once
+// (one at a time: packed prompts 40 us, one query 137 us; so 37 and 135).
 template <int D>
 __global__ void __launch_bounds__(256) attend_dense_join_kernel(
     const float* __restrict__ part, const float2* __restrict__ part_ml, int nq, int nsplit,
@@ -700,8 +717,9 @@ __global__ void __launch_bounds__(256) attend_dense_join_kernel(
   if (lane == 0 && lse != nullptr) lse[r] = (m + log2f(l)) * kLn2;
 }
 
-// Slices of the key tiles per query tile: the count with the least estimated time on 148
-// SMs, one CTA each.  A tile is taken as 1 unit, a CTA's start and end as 4, the join kernel as 5 plus the partial sums' traffic.
+// Slices of the key tiles per query tile: the count with the least estimated time on 148 SMs, one
+// CTA each.  A tile (0.9 us) is taken as 1 unit, a CTA's start and end as 4, the join kernel as 5
+// plus the partial sums' traffic.
 int attend_dense_splits(int H, int nq, int nk, int nc, int d) {
   constexpr int kSms = 148;
   const long long qt = (static_cast<long long>(nq) + 127) / 128;
@@ -799,6 +817,8 @@ cudaError_t launch_attend_dense(const DenseMaps& maps, int H, int nq, int nk, in
 
 // ------------------------------------------------------------------------------ key ranges
 
+// One thread per row, a binary search over the segments' offsets (which stay in L1) and one
+// 16-byte store: bound by latency.
 // Row i of segment b (the one whose queries q_offsets[b] .. q_offsets[b+1]-1 hold i): the whole
 // of the segment's video keys and of its context keys, the latter ended at
 // max(prefix_b, i - first + 1 + context - queries) when causal.  Rows of no segment are empty.

@@ -69,8 +69,8 @@ __device__ __forceinline__ void cp_wait() {
 // V: values per access (the two halves of V pairs are V values each); C: such accesses per
 // thread and half.
 template <typename T, int D, int V, int C>
-__global__ void __launch_bounds__(kRopeThreads, kRopeCtas) qk_norm_rope_kernel(const RopeArgs a,
-                                                                    int heads_per_cta) {
+__global__ void __launch_bounds__(kRopeThreads, kRopeCtas)
+    qk_norm_rope_kernel(const RopeArgs a, int heads_per_cta) {
   constexpr int kLanes = D / 2 / (V * C);          // threads per row
   constexpr int kTokens = kRopeThreads / kLanes;   // tokens per CTA
   using Vt = Vec<T, V>;
@@ -247,8 +247,8 @@ static int rope_vec(const RopeArgs& a, int esize, int d) {
     for (int t = 0; t < 3; ++t) {
       if (a.in[t] == nullptr) continue;
       const uintptr_t bytes = static_cast<uintptr_t>(n) * esize;
-      if (reinterpret_cast<uintptr_t>(a.in[t]) % bytes || reinterpret_cast<uintptr_t>(a.out[t]) % bytes)
-        return false;
+      const uintptr_t in = reinterpret_cast<uintptr_t>(a.in[t]);
+      if (in % bytes || reinterpret_cast<uintptr_t>(a.out[t]) % bytes) return false;
       if (a.head_stride[t] % n || a.token_stride[t] % n) return false;
     }
     return true;

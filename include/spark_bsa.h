@@ -234,7 +234,8 @@ SPARK_API spark_status spark_bsa_attend(const void* Qp, const void* Kp, const vo
  * as the exact and compressed branches (logit sigma q.kc_j).  They form no block and take no
  * part in the anchor, the block means, the summaries or the routing; k is still taken over the
  * nkb video blocks.  Context queries are not part of this operation (spark_attend_dense attends
- * them, spark_bsa_forward_joint runs both).  0 <= nc <= SPARK_MAX_NC; nc == 0 is exactly the call without context. */
+ * them, spark_bsa_forward_joint runs both).  0 <= nc <= SPARK_MAX_NC; nc == 0 is exactly the call
+ * without context. */
 
 /* Workspace bytes spark_bsa_forward_ctx needs: spark_bsa_workspace_size plus two bf16
  * [H,nc,d] regions (each rounded up to 256 bytes) that receive the converted context rows at
