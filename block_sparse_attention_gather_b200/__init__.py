@@ -16,7 +16,12 @@ perm[offsets[i]:offsets[i+1]]) and block offsets [nb + 1] int32 (1..128 tokens p
 ``spark_reblock(Q, K, block=128)`` returns (q_perm, k_perm, offsets).  Variants:
 - ``spark_bsa_forward_ctx`` adds always-exact context (sink) rows;
 - ``spark_bsa_forward_fp8`` takes the logit product in e4m3;
-- ``spark_bsa_forward_host`` runs from host buffers with the copies overlapped.
+- ``spark_bsa_forward_host`` runs from host buffers with the copies overlapped;
+- ``spark_bsa_forward_joint`` also attends the context queries.
+
+Around the sparse call: ``spark_qk_norm_rope`` (per-head norm and rotation of Q and K, laid out
+with V), ``spark_attend_dense`` (dense attention over video and context keys under per-row key
+ranges) and ``spark_attend_ranges`` (those ranges from segment offsets).
 
 The step entry points (``spark_bsa_gather_q``, ``spark_bsa_anchor``,
 ``spark_bsa_gather_kv_summarize``, ``spark_bsa_route``, ``spark_bsa_attend`` and the comparator
