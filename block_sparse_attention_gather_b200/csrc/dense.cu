@@ -138,14 +138,21 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
   return d;
 }
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
 // 2^a of two values without the special-function unit: 2^a = 2^n 2^f, n the nearest integer
 // (taken by adding 1.5 * 2^23, which leaves n in the low bits), 2^f on [-1/2, 1/2] by a degree-4
 // polynomial fitted for the least largest relative error (2.7e-6 in fp32; the result is rounded
-// to bf16, 2^-9).  Arguments under -126 give 2^-126 and NaN gives a number: the caller's other
-// values of the row carry a NaN.
-__device__ __forceinline__ void ex2_poly2(uint64_t a2, float& p0, float& p1) {
+// to bf16, 2^-9).  Arguments under -126 give 2^-126.  Those from 128 on and NaN give anything:
+// `top`, the largest argument so far, tells the caller.
+__device__ __forceinline__ void ex2_poly2(uint64_t a2, float& top, float& p0, float& p1) {
   float a0, a1;
   f2_unpack(a2, a0, a1);
+  top = max3_nan(top, a0, a1);
   a2 = f2_pack(fmaxf(a0, -126.f), fmaxf(a1, -126.f));
   const uint64_t r2 = f2_add(a2, f2_splat(12582912.f));
   const uint64_t f2 = f2_fma(f2_add(r2, f2_splat(-12582912.f)), f2_splat(-1.f), a2);
@@ -200,25 +207,21 @@ __device__ __forceinline__ uint32_t bits32(int lo, int hi) {
   return below(hi) & ~below(lo);
 }
 
-// p of 32 scores (raw; those whose bit of `live` is clear masked when kExact) as packed bf16
-// pairs; returns their sum (two partial ones).  kExact: every exponential by the special-function
-// unit, so that a masked place is an exact zero; otherwise one pair in kPolyEvery by the
-// polynomial.
-template <bool kExact>
-__device__ __forceinline__ uint64_t exp32(const uint32_t (&r)[32], uint32_t live, uint64_t c2,
-                                          uint64_t nm2, uint32_t (&pk)[16]) {
+// p of 32 scores (raw) as packed bf16 pairs; returns their sum (two partial ones).  One pair in
+// kPolyEvery takes the polynomial (its largest argument goes to `top`), the others the
+// special-function unit.  A masked score (-inf) gives 0 or, by the polynomial, 2^-126, which no
+// row with a live key notices (one attains the reference, so l >= 1); a row without one is known
+// by its reference.
+__device__ __forceinline__ uint64_t exp32(const uint32_t (&r)[32], uint64_t c2, uint64_t nm2,
+                                          float& top, uint32_t (&pk)[16]) {
   uint64_t sum2[2] = {0, 0};
 #pragma unroll
   for (int j = 0; j < 16; ++j) {
-    float x0 = __uint_as_float(r[2 * j]), x1 = __uint_as_float(r[2 * j + 1]);
-    if (kExact) {
-      if (!(live & (1u << (2 * j)))) x0 = -INFINITY;
-      if (!(live & (2u << (2 * j)))) x1 = -INFINITY;
-    }
-    const uint64_t a2 = f2_fma(f2_pack(x0, x1), c2, nm2);
+    const uint64_t a2 = f2_fma(f2_pack(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1])),
+                               c2, nm2);
     float p0, p1;
-    if (!kExact && j % kPolyEvery == kPolyEvery - 1) {
-      ex2_poly2(a2, p0, p1);
+    if (j % kPolyEvery == kPolyEvery - 1) {
+      ex2_poly2(a2, top, p0, p1);
     } else {
       float a0, a1;
       f2_unpack(a2, a0, a1);
@@ -230,12 +233,11 @@ __device__ __forceinline__ uint64_t exp32(const uint32_t (&r)[32], uint32_t live
   return f2_add(sum2[0], sum2[1]);
 }
 
-// The tile's 128 scores at `sbuf` -> packed pairs, returning the sum of p; columns outside
-// [lo, hi) are masked when kExact.  The load of the second half's columns is in flight while the
-// first half's are exponentiated.
-template <bool kExact>
-__device__ __forceinline__ float exp_tile(uint32_t sbuf, int lo, int hi, float c, float m,
-                                          uint32_t (&pk)[4][16]) {
+// The tile's 128 scores at `sbuf` -> packed pairs, returning the sum of p, which is no number
+// under 2^24 when a score is NaN or its p reaches that.  The load of the second half's columns is
+// in flight while the first half's are exponentiated.
+__device__ __forceinline__ float exp_tile(uint32_t sbuf, float c, float m, uint32_t (&pk)[4][16]) {
+  float top = -INFINITY;
   const uint64_t c2 = f2_splat(c), nm2 = f2_splat(-m);
   uint32_t r[4][32];
   tmem_ld32_issue(sbuf, r[0]);
@@ -244,28 +246,46 @@ __device__ __forceinline__ float exp_tile(uint32_t sbuf, int lo, int hi, float c
   tmem_wait32(r[1]);
   tmem_ld32_issue(sbuf + 64, r[2]);
   tmem_ld32_issue(sbuf + 96, r[3]);
-  uint64_t s = exp32<kExact>(r[0], kExact ? bits32(lo, hi) : 0u, c2, nm2, pk[0]);
-  s = f2_add(s, exp32<kExact>(r[1], kExact ? bits32(lo - 32, hi - 32) : 0u, c2, nm2, pk[1]));
+  uint64_t s = exp32(r[0], c2, nm2, top, pk[0]);
+  s = f2_add(s, exp32(r[1], c2, nm2, top, pk[1]));
   tmem_wait32(r[2]);
   tmem_wait32(r[3]);
-  s = f2_add(s, exp32<kExact>(r[2], kExact ? bits32(lo - 64, hi - 64) : 0u, c2, nm2, pk[2]));
-  s = f2_add(s, exp32<kExact>(r[3], kExact ? bits32(lo - 96, hi - 96) : 0u, c2, nm2, pk[3]));
+  s = f2_add(s, exp32(r[2], c2, nm2, top, pk[2]));
+  s = f2_add(s, exp32(r[3], c2, nm2, top, pk[3]));
   float s0, s1;
   f2_unpack(s, s0, s1);
-  return s0 + s1;
+  return top < 120.f ? s0 + s1 : INFINITY;
 }
 
-// Maximum of the tile's scores (raw) of columns [lo, hi), NaN if one is; -inf if there is none.
-__device__ __forceinline__ float max_tile(uint32_t sbuf, int lo, int hi) {
+// Sets the tile's scores outside columns [lo, hi) to -inf where they stand (a pass of its own, so
+// that the exponentials have one form: with a second, masking one the loop outgrew the
+// instruction caches).
+__device__ __forceinline__ void mask_tile(uint32_t sbuf, int lo, int hi) {
+#pragma unroll 1
+  for (int cc = 0; cc < 128; cc += 32) {
+    uint32_t r[32], q[16];
+    tmem_ld32(sbuf + cc, r);
+    const uint32_t live = bits32(lo - cc, hi - cc);
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+#pragma unroll
+      for (int j = 0; j < 16; ++j)
+        q[j] = live & (1u << (16 * half + j)) ? r[16 * half + j] : 0xff800000u;
+      tmem_st16_issue(sbuf + cc + 16 * half, q);
+    }
+  }
+  tmem_wait_st();
+}
+
+// Maximum of the tile's scores (raw), NaN if one is.
+__device__ __forceinline__ float max_tile(uint32_t sbuf) {
   float mx = -INFINITY;
 #pragma unroll 1
   for (int cc = 0; cc < 128; cc += 32) {
     uint32_t r[32];
     tmem_ld32(sbuf + cc, r);
-    const uint32_t live = bits32(lo - cc, hi - cc);
 #pragma unroll
-    for (int j = 0; j < 32; ++j)
-      if (live & (1u << j)) mx = max_nan(mx, __uint_as_float(r[j]));
+    for (int j = 0; j < 32; ++j) mx = max_nan(mx, __uint_as_float(r[j]));
   }
   return mx;
 }
@@ -487,10 +507,11 @@ __global__ void __launch_bounds__(kThreads, 1) attend_dense_kernel(
       float mx = -INFINITY;
       if (grp < T && (ok = wait_s(grp)) && warp_live) {
         tc_fence_after_sync();
+        const uint32_t sbuf = tbase + lane_off + grp * 128;
         const int y = tl.row(grp);
         const bool video = tl.video(grp);
-        mx = c * max_tile(tbase + lane_off + grp * 128, (video ? rg.x : rg.z) - y,
-                          (video ? rg.y : rg.w) - y);
+        mask_tile(sbuf, (video ? rg.x : rg.z) - y, (video ? rg.y : rg.w) - y);
+        mx = c * max_tile(sbuf);
       }
       first_max[grp][row] = mx;
       named_bar_sync(1 + q4, 64);                          // the two groups of this quarter
@@ -514,12 +535,11 @@ __global__ void __launch_bounds__(kThreads, 1) attend_dense_kernel(
 #pragma unroll
           for (int j = 0; j < 16; ++j) pk[i][j] = 0u;
       } else {
-        const bool edge = __any_sync(kAll, lo > 0 || hi < 128);
+        if (__any_sync(kAll, lo > 0 || hi < 128)) mask_tile(sbuf, lo, hi);
         float sum;
         for (int pass = 0;; ++pass) {
-          const float m = ref == -INFINITY ? 0.f : ref;    // no live key yet: every p is 0
-          sum = edge || pass > 0 ? exp_tile<true>(sbuf, lo, hi, c, m, pk)
-                                 : exp_tile<false>(sbuf, lo, hi, c, m, pk);
+          // no live key yet: every p is (next to) 0
+          sum = exp_tile(sbuf, c, ref == -INFINITY ? 0.f : ref, pk);
           if (pass == 0) {
             // The other group hands its tile over first; it may have raised the reference, which
             // what is here then has to follow.
@@ -535,7 +555,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_dense_kernel(
           // the reference is too low, or a row sees its first keys without one
           if (pass == 2 || !__any_sync(kAll, !(sum < kMaxSum) || (ref == -INFINITY && some)))
             break;
-          const float mx = max_tile(sbuf, lo, hi) * c;
+          const float mx = max_tile(sbuf) * c;
           const bool grow = !(mx <= ref);                  // a NaN among the scores too
           // a score of +inf leaves no number to compare the others with
           const float next = grow ? (mx < INFINITY ? mx : NAN) : ref;
@@ -597,7 +617,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_dense_kernel(
       const size_t prow = (static_cast<size_t>(h) * nsplit + split) * nq + qi;
       // one slice: the output; several: unnormalised partial sums for the join
       const float inv = nsplit > 1 ? 1.f : 1.f / l;
-      const bool none = l == 0.f;                          // no live key: zeros
+      const bool none = ref == -INFINITY;                  // no live key: zeros
 #pragma unroll
       for (int cc = 0; cc < D / 2; cc += 32) {
         const int col = grp * (D / 2) + cc;
@@ -633,7 +653,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_dense_kernel(
         if (nsplit > 1)
           part_ml[prow] = make_float2(ref, l);
         else if (lse != nullptr)
-          lse[at] = (ref + log2f(l)) * kLn2;
+          lse[at] = none ? -INFINITY : (ref + log2f(l)) * kLn2;
       }
     }
   }
@@ -674,8 +694,8 @@ __global__ void __launch_bounds__(256) attend_dense_join_kernel(
   float w[2], l = 0.f, acc[kPer] = {};
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    // a slice without a live key has l = 0 and zeros
-    w[i] = ml[i].y == 0.f ? 0.f : ex2_approx(ml[i].x - m);
+    // a slice without a live key has no reference, and zeros
+    w[i] = ml[i].x == -INFINITY ? 0.f : ex2_approx(ml[i].x - m);
     ml[i].y *= w[i];
   }
   for (int s0 = 0; s0 < nsplit; s0 += 8) {

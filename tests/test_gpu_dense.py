@@ -194,6 +194,38 @@ def test_nan_in_a_live_key_reaches_its_rows_only():
     assert ((out[0, 1].double() - ref[0, 1]).abs() <= 2.0 ** -7 * A[0, 1] + 1e-6).all()
 
 
+@pytest.mark.parametrize("nats", [20, 60, 88, 100, 150, 200])
+@pytest.mark.parametrize("tile", [0, 1, 4])
+@pytest.mark.parametrize("far", [1, -1])
+def test_one_key_far_above_the_others(nats, tile, far):
+    """Row i's own key, at column i of the tile, exceeds all it saw before by up to 289 powers of
+    two (or is that far below): every column of a tile, whatever computes its exponential."""
+    H, n, d = 1, 900, 128
+    g = torch.Generator(device=DEV).manual_seed(nats)
+    eye = torch.eye(128, device=DEV)
+    Q = (16 * eye)[None].to(BF)
+    K = torch.zeros(H, n, d, device=DEV)
+    K[:, 128 * tile:128 * tile + 128] = far * nats * math.sqrt(128) / 16 * eye
+    x = dict(Q=Q, K=K.to(BF), V=torch.randn(H, n, d, generator=g, device=DEV).to(BF), Kc=None,
+             Vc=None)
+    out, lse = spark_attend_dense(**x, out_dtype=torch.float32)
+    # one product per score, exact in fp32 but for its scale: 2^-22 of 200 is under 2^-14
+    check(x, out, lse)
+
+
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+@pytest.mark.parametrize("tile", [0, 1, 3])
+def test_bad_score_at_every_column(bad, tile):
+    x = inputs(16, 1, 3, 700, 0, 128)
+    x["Q"] = x["Q"].abs() + 0.5
+    keep = x["K"].clone()
+    for j in range(128):
+        x["K"] = keep.clone()
+        x["K"][0, 128 * tile + j] = bad
+        out, lse = spark_attend_dense(**x)
+        assert torch.isnan(out).all() and torch.isnan(lse).all(), j
+
+
 def test_keys_past_32_bit_offsets():
     """4.6 GB of keys: byte and element offsets beyond 2^32 and 2^31."""
     H, nk, d = 3, 6_000_000, 128
