@@ -213,6 +213,24 @@ def test_one_key_far_above_the_others(nats, tile, far):
     check(x, out, lse)
 
 
+@pytest.mark.parametrize("nats", [20, 88, 100, 150])
+@pytest.mark.parametrize("tile", [0, 1, 3])
+def test_one_row_alone_meets_a_far_key(nats, tile):
+    """As above with nothing else in the row's warp that would have the tile looked at again."""
+    d, n = 128, 600
+    g = torch.Generator(device=DEV).manual_seed(nats)
+    V = torch.randn(1, n, d, generator=g, device=DEV).to(BF)
+    Q = torch.zeros(1, 1, d, device=DEV)
+    Q[..., 0] = 16
+    Q = Q.to(BF)
+    for j in range(128):
+        K = torch.zeros(1, n, d, device=DEV)
+        K[0, 128 * tile + j, 0] = nats * math.sqrt(128) / 16
+        K = K.to(BF)
+        out, lse = spark_attend_dense(Q, K, V, out_dtype=torch.float32)
+        check(dict(Q=Q, K=K, V=V, Kc=None, Vc=None), out, lse)
+
+
 @pytest.mark.parametrize("bad", [math.nan, math.inf])
 @pytest.mark.parametrize("tile", [0, 1, 3])
 def test_bad_score_at_every_column(bad, tile):
