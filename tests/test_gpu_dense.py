@@ -337,6 +337,24 @@ def test_two_streams_at_once():
         assert all(torch.equal(o, w[0]) and torch.equal(l, w[1]) for o, l in g)
 
 
+@pytest.mark.parametrize("H,nq,nk", [(2, 7, 9000), (8, 300, 300), (1, 128, 128)])
+def test_calls_that_feed_each_other(H, nq, nk):
+    """Each call's output is the next one's queries, in the same buffers: kernels may be set up
+    before the one ahead of them ends, but must not read or write ahead of it."""
+    x = inputs(60, H, nq, nk, 33, 128)
+    size = spark_attend_dense_workspace_size(H, nq, nk, 33, 128)
+    ws = torch.empty(size, dtype=torch.uint8, device=DEV)
+    q, outs = x.pop("Q"), []
+    for sync in (True, False):
+        bufs = [q.clone(), torch.empty_like(q)]
+        for i in range(30):
+            spark_attend_dense(bufs[i % 2], **x, out=bufs[(i + 1) % 2], workspace=ws)
+            if sync:
+                torch.cuda.synchronize()
+        outs.append(bufs[0].clone())
+    assert torch.equal(outs[0], outs[1])
+
+
 @pytest.mark.parametrize("nq", [5, 300])
 def test_expired_wait_is_flagged_and_leaves_the_context_usable(nq):
     x = inputs(14, 2, nq, 3000, 10, 128)
