@@ -28,20 +28,21 @@
 // not matter; rows of V outside the ranges of the whole query tile are zeroed in shared memory
 // before the product, as 0 * NaN would not be 0.
 //
-// What bounds it.  Few rows: reading K and V once (24 heads x 60480 keys, one row: 127 us =
-// 5.9 TB/s); the keys are split over the SMs and joined.  Many rows: the exponentials, with the
+// What bounds it.  Few rows: reading K and V once (24 heads x 60480 keys, one row: 109 us =
+// 6.8 TB/s, and 4 us for the join of the slices that the keys are split into).  Many rows: the exponentials, with the
 // tensor pipe at 63% of its cycles next to them.  Two softmax warps share a scheduler and take
 // about 1700 cycles a tile each, of which 700 are the special-function unit's (88 of the 128
 // exponentials of a row's tile; the others by polynomial) and the rest the latencies of some 700
 // instructions in order; the MMAs of a tile take 1024 cycles, and reading Q, K, V and writing K, V
-// in shared memory 1280.  24 heads x 30240 x 30240 take 9.05 ms alone (1241 TFLOP/s) and 10.0 ms
-// in a loop at the 1000 W power cap (1120 TFLOP/s at 1470 MHz).
+// in shared memory 1280.  24 heads x 30240 x 30240 take 9.05 ms alone (1241 TFLOP/s) and 9.8 ms
+// in a loop at the 1000 W power cap (1145 TFLOP/s, 1470 MHz).
 //
 // The steps, on that case unless named: running maximum, pair of query tiles per CTA 10.9 ms;
 // no maximum per tile 10.3; registers moved to the softmax warps, polynomial 9.7; tile waits in a
 // warp of their own 9.3 (a barrier test takes a few hundred cycles while the MMAs read shared
 // memory); one query tile per CTA, three S buffers, common reference 9.5 against 10.6 on one box,
-// and packed prompts 58 -> 40 us; late query tiles first 285 -> 272 us (8191 causal rows).
+// and packed prompts 58 -> 40 us; late query tiles first 285 -> 272 us (8191 causal rows); masks
+// over the scores instead of in the exponentials 10.0 -> 9.7.
 // Measured and not kept: S in 64-key units (an M = 128 MMA takes 64 cycles for N = 64 too), P
 // handed over in halves, CTA pairs with M = 256 (no faster: the exponentials bound both).
 //
@@ -49,7 +50,6 @@
 // copies and MMAs, frees TMEM and returns.
 #include <atomic>
 #include <climits>
-#include <type_traits>
 
 #include "spark_kernels.cuh"
 
