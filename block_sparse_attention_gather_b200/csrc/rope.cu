@@ -18,6 +18,8 @@
 // three tensors in a thread, loads into registers), 401 us (one tensor per CTA), 380 us
 // (accesses that cover whole sectors), 333 us (asynchronous copies) and 299 us = 6.2 TB/s
 // (streaming stores, 6 CTAs of 128 threads an SM), 95% of the measured copy bandwidth.
+#include <type_traits>
+
 #include "spark_kernels.cuh"
 
 namespace spark {
@@ -67,8 +69,10 @@ __device__ __forceinline__ void cp_wait() {
 }  // namespace
 
 // V: values per access (the two halves of V pairs are V values each); C: such accesses per
-// thread and half.
-template <typename T, int D, int V, int C>
+// thread and half; kPart: some vector of an interleaved row is rotated in part, which takes a test
+// per pair (with the test in every row 60480 tokens took 325 us in place of 306; without vectors
+// rotated in part, by narrower accesses, 16384 tokens with 33 pairs took 75 us in place of 40).
+template <typename T, int D, int V, int C, bool kPart>
 __global__ void __launch_bounds__(kRopeThreads, kRopeCtas)
     qk_norm_rope_kernel(const RopeArgs a, int heads_per_cta) {
   constexpr int kLanes = D / 2 / (V * C);          // threads per row
@@ -87,7 +91,9 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas)
   // of one pair.
   constexpr int kInner = V > 1 ? V / 2 : 1;        // whole pairs in a vector
   int col[C][2];
-  bool rot[C][2];                                  // half layout: rot[.][0] alone counts
+  // whether each vector is rotated (half layout and V = 1: rot[.][0] counts for both), or with
+  // kPart how many of its pairs are
+  std::conditional_t<kPart, int, bool> rot[C][2];
   float cs[C][V], sn[C][V], w[C][2][V];
   const bool half = !a.interleaved && a.pairs > 0;
 #pragma unroll
@@ -103,12 +109,18 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas)
       col[c][0] = p, col[c][1] = p + D / 2;
       rot[c][0] = t < 2 && col[c][0] < 2 * a.pairs;
       rot[c][1] = t < 2 && col[c][1] < 2 * a.pairs;
+      if constexpr (kPart) {
+        rot[c][0] *= min(kInner, a.pairs - col[c][0] / 2);
+        rot[c][1] *= min(kInner, a.pairs - col[c][1] / 2);
+      }
     }
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       cs[c][j] = sn[c][j] = 0.f;
       const int e = half || V == 1 ? 0 : j / kInner;
-      if (rot[c][e] && live) {
+      bool here = rot[c][e] && live;
+      if constexpr (kPart) here = here && j % kInner < rot[c][e];
+      if (here) {
         const int i = half || V == 1 ? p + j : col[c][e] / 2 + j % kInner;
         int axis = 0;
         for (int k = 1; k < a.naxes; ++k) axis += i >= a.first[k];
@@ -199,6 +211,9 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas)
             if (!rot[c][e]) continue;
 #pragma unroll
             for (int i = 0; i < kInner; ++i) {
+              if constexpr (kPart) {
+                if (i >= rot[c][e]) break;
+              }
               const int j = e * kInner + i;
               const float p = y[e * V + 2 * i], q = y[e * V + 2 * i + 1];
               y[e * V + 2 * i] = p * cs[c][j] - q * sn[c][j];
@@ -234,8 +249,10 @@ static cudaError_t launch_rope_t(const RopeArgs& a, cudaStream_t s) {
   int splits = static_cast<int>((kRopeCtas * 148 + ctas - 1) / ctas);
   if (splits > a.H) splits = a.H;
   const int per = (a.H + splits - 1) / splits;
-  qk_norm_rope_kernel<T, D, V, C>
-      <<<dim3(blocks, (a.H + per - 1) / per, tensors), kRopeThreads, 0, s>>>(a, per);
+  const auto kern = V > 1 && a.interleaved && a.pairs % (V > 1 ? V / 2 : 1) != 0
+                        ? qk_norm_rope_kernel<T, D, V, C, (V > 1)>
+                        : qk_norm_rope_kernel<T, D, V, C, false>;
+  kern<<<dim3(blocks, (a.H + per - 1) / per, tensors), kRopeThreads, 0, s>>>(a, per);
   return cudaGetLastError();
 }
 
@@ -243,7 +260,8 @@ static cudaError_t launch_rope_t(const RopeArgs& a, cudaStream_t s) {
 static int rope_vec(const RopeArgs& a, int esize, int d) {
   int v = esize == 2 ? 8 : 4;
   auto fits = [&](int n) {
-    if (a.pairs % n != 0 || (d / 2) % n != 0) return false;   // no vector half rotated
+    // the two sides of a half layout's pairs have to start at whole vectors
+    if ((!a.interleaved && a.pairs % n != 0) || (d / 2) % n != 0) return false;
     for (int t = 0; t < 3; ++t) {
       if (a.in[t] == nullptr) continue;
       const uintptr_t bytes = static_cast<uintptr_t>(n) * esize;

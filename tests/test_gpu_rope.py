@@ -135,6 +135,25 @@ def test_in_place_and_on_another_stream(interleaved):
         assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("shift", [0, 2])
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("dtype", [BF, torch.float32])
+def test_every_count_of_pairs_and_what_lies_behind_them(dtype, interleaved, shift):
+    base = torch.randn(9 * 128 + 8, device=DEV).to(dtype)
+    pos = torch.tensor([5, -7, 100], device=DEV, dtype=torch.int32)[:, None]
+    for pairs in range(1, 65):
+        x = base.clone()[shift:shift + 9 * 128].view(3, 3, 128)
+        if shift == 0 and pairs < 64:
+            x[..., 2 * pairs:] = torch.tensor([float("inf"), float("nan")], device=DEV,
+                                              dtype=dtype).repeat(64 - pairs)
+        freq = spark_rope_frequencies([pairs])[0].to(DEV)
+        got = spark_qk_norm_rope(x, None, None, None, None, 1e-6, pos, freq, [pairs], interleaved)[0]
+        assert torch.equal(got[..., 2 * pairs:].nan_to_num(7.0), x[..., 2 * pairs:].nan_to_num(7.0))
+        ones = torch.where(torch.isfinite(x), x, torch.ones_like(x))
+        want = reference(ones, None, 1e-6, pos, freq, [pairs], interleaved, 1.0)
+        check(got[..., :2 * pairs], [t[..., :2 * pairs] for t in want])
+
+
 def test_inputs_that_repeat_themselves():
     """Strides of 0: one head shared by all (Q), one token by all (K)."""
     H, N, d = 5, 60, 128
