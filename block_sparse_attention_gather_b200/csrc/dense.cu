@@ -29,13 +29,13 @@
 // before the product, as 0 * NaN would not be 0.
 //
 // What bounds it.  Few rows: reading K and V once (24 heads x 60480 keys, one row: 109 us =
-// 6.8 TB/s, and 4 us for the join of the slices that the keys are split into).  Many rows: the exponentials, with the
-// tensor pipe at 63% of its cycles next to them.  Two softmax warps share a scheduler and take
-// about 1700 cycles a tile each, of which 700 are the special-function unit's (88 of the 128
-// exponentials of a row's tile; the others by polynomial) and the rest the latencies of some 700
-// instructions in order; the MMAs of a tile take 1024 cycles, and reading Q, K, V and writing K, V
-// in shared memory 1280.  24 heads x 30240 x 30240 take 9.05 ms alone (1241 TFLOP/s) and 9.8 ms
-// in a loop at the 1000 W power cap (1145 TFLOP/s, 1470 MHz).
+// 6.8 TB/s, and 4 us for the join of the slices that the keys are split into).  Many rows: the
+// exponentials, with the tensor pipe at 63% of its cycles.  Two softmax warps share a scheduler
+// and take about 1700 cycles a tile each, of which 700 are the special-function unit's (88 of the
+// 128 exponentials of a row's tile; the others by polynomial) and the rest the latencies of some
+// 700 instructions in order; the MMAs of a tile take 1024 cycles, and reading Q, K, V and writing
+// K, V in shared memory 1280.  24 heads x 30240 x 30240 take 9.05 ms alone (1241 TFLOP/s) and
+// 9.8 to 10.0 ms in a loop at the 1000 W power cap (1126 to 1147 TFLOP/s, 1470 MHz).
 //
 // The steps, on that case unless named: running maximum, pair of query tiles per CTA 10.9 ms;
 // no maximum per tile 10.3; registers moved to the softmax warps, polynomial 9.7; tile waits in a
