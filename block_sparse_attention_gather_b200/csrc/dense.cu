@@ -146,20 +146,21 @@ __device__ __forceinline__ float max3_nan(float a, float b, float c) {
 
 // 2^a of two values without the special-function unit: 2^a = 2^n 2^f, n the nearest integer
 // (taken by adding 1.5 * 2^23, which leaves n in the low bits), 2^f on [-1/2, 1/2] by a degree-4
-// polynomial fitted for the least largest relative error (2.7e-6 in fp32; the result is rounded
-// to bf16, 2^-9).  Arguments under -126 give 2^-126.  Those from 128 on and NaN give anything:
-// `top`, the largest argument so far, tells the caller.
+// polynomial that is 1 at 0, fitted for the least largest relative error (2.9e-6 in fp32; the result
+// is rounded to bf16, 2^-9).  Arguments from -127 down give 0 exactly (n = -127 takes the exponent of
+// 1.0 away), so that a masked key adds none of its value, however large.  Those from 128 on and NaN
+// give anything: `top`, the largest argument so far, tells the caller.
 __device__ __forceinline__ void ex2_poly2(uint64_t a2, float& top, float& p0, float& p1) {
   float a0, a1;
   f2_unpack(a2, a0, a1);
   top = max3_nan(top, a0, a1);
-  a2 = f2_pack(fmaxf(a0, -126.f), fmaxf(a1, -126.f));
+  a2 = f2_pack(fmaxf(a0, -127.f), fmaxf(a1, -127.f));
   const uint64_t r2 = f2_add(a2, f2_splat(12582912.f));
   const uint64_t f2 = f2_fma(f2_add(r2, f2_splat(-12582912.f)), f2_splat(-1.f), a2);
-  uint64_t y = f2_fma(f2_splat(0.009570101906375769f), f2, f2_splat(0.05591786031900944f));
-  y = f2_fma(y, f2, f2_splat(0.2402474482798183f));
-  y = f2_fma(y, f2, f2_splat(0.6931218147367589f));
-  y = f2_fma(y, f2, f2_splat(0.9999992614456781f));
+  uint64_t y = f2_fma(f2_splat(0.009585382416844368f), f2, f2_splat(0.05590662732720375f));
+  y = f2_fma(y, f2, f2_splat(0.24024038016796112f));
+  y = f2_fma(y, f2, f2_splat(0.6931241750717163f));
+  y = f2_fma(y, f2, f2_splat(1.f));
   float y0, y1, r0, r1;
   f2_unpack(y, y0, y1);
   f2_unpack(r2, r0, r1);
@@ -209,9 +210,8 @@ __device__ __forceinline__ uint32_t bits32(int lo, int hi) {
 
 // p of 32 scores (raw) as packed bf16 pairs; returns their sum (two partial ones).  One pair in
 // kPolyEvery takes the polynomial (its largest argument goes to `top`), the others the
-// special-function unit.  A masked score (-inf) gives 0 or, by the polynomial, 2^-126, which no
-// row with a live key notices (one attains the reference, so l >= 1); a row without one is known
-// by its reference.
+// special-function unit.  A masked score (-inf) gives 0; a row without a live key is known by its
+// reference.
 __device__ __forceinline__ uint64_t exp32(const uint32_t (&r)[32], uint64_t c2, uint64_t nm2,
                                           float& top, uint32_t (&pk)[16]) {
   uint64_t sum2[2] = {0, 0};

@@ -183,6 +183,29 @@ def test_masked_places_may_hold_anything(nq, d, bad):
     check(x, out, lse, r)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_masked_values_as_large_as_the_type_holds(d):
+    """Keys that some rows of a tile see and others mask, with values up to bf16's largest: nothing of
+    them may reach the rows that mask them."""
+    x = inputs(17, 2, 300, 700, 130, d)
+    r = torch.zeros(300, 4, dtype=torch.int32, device=DEV)
+    r[:, 1], r[:, 3] = 500, 60
+    r[::2] = torch.tensor([200, 700, 60, 130], device=DEV, dtype=torch.int32)
+    large = torch.finfo(BF).max
+    x["V"][:, 500:], x["Vc"][:, 60:] = large / 2 ** 20, -large / 2 ** 20
+    x["V"][:, :200], x["Vc"][:, :60] = large, -large       # the even rows' masked keys
+    out, lse = spark_attend_dense(**x, ranges=r, out_dtype=torch.float32)
+    for t, n in (("V", 200), ("Vc", 60)):
+        x[t][:, :n] = 0
+    even = dict(x, Q=x["Q"][:, ::2].contiguous())
+    check(even, out[:, ::2], lse[:, ::2], r[::2].contiguous())
+    x["V"][:, 500:], x["Vc"][:, 60:] = large, -large       # and the odd rows'
+    out, lse = spark_attend_dense(**x, ranges=r, out_dtype=torch.float32)
+    x["V"][:, 500:], x["Vc"][:, 60:] = 0, 0
+    odd = dict(x, Q=x["Q"][:, 1::2].contiguous())
+    check(odd, out[:, 1::2], lse[:, 1::2], r[1::2].contiguous())
+
+
 def test_nan_in_a_live_key_reaches_its_rows_only():
     x = inputs(9, 1, 2, 600, 0, 128)
     x["K"][0, 500] = math.nan
