@@ -25,8 +25,9 @@
 // and raise it itself.
 //
 // Keys beyond a row's ranges are masked to -inf by value, so what they hold (NaN included) does
-// not matter; rows of V outside the ranges of the whole query tile are zeroed in shared memory
-// before the product, as 0 * NaN would not be 0.
+// not matter; rows of V that no row of the query tile sees are zeroed in shared memory before the
+// product, as 0 * NaN would not be 0: those past the hull of the ranges, and, where the ranges of
+// neighbouring rows do not touch (padding between segments), those in the gaps.
 //
 // What bounds it.  Few rows: reading K and V once (24 heads x 60480 keys, one row: 109 us =
 // 6.8 TB/s, and 4 us for the join of the slices that the keys are split into).  Many rows: the
@@ -290,6 +291,11 @@ __device__ __forceinline__ float max_tile(uint32_t sbuf) {
   return mx;
 }
 
+// Whether two ranges leave keys between them (they neither overlap nor touch).
+__device__ __forceinline__ bool apart(int a0, int a1, int b0, int b1) {
+  return a0 < a1 && b0 < b1 && (b0 > a1 || a0 > b1);
+}
+
 }  // namespace
 
 template <int D>
@@ -311,7 +317,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_dense_kernel(
   uint8_t* ring = qst + C::kTile;
   __shared__ Bars<kStages> bars;
   __shared__ int s_skip;
-  __shared__ int hull[8][4];
+  __shared__ int hull[8][4], hull_gaps[8];
   __shared__ float row_ref[128];             // the rows' reference as of the last tile handed over
   __shared__ float first_max[2][128];        // the rows' maxima of each group's first tile
   // sums of the groups' rows, over the query tile once every MMA has read it
@@ -343,7 +349,17 @@ __global__ void __launch_bounds__(kThreads, 1) attend_dense_kernel(
     }
     const int a = __reduce_min_sync(kAll, r.x), b = __reduce_max_sync(kAll, r.y);
     const int c = __reduce_min_sync(kAll, r.z), e = __reduce_max_sync(kAll, r.w);
+    // Whether this row's ranges and those of the last row before it that has any leave keys
+    // between them: where none do, the rows see every key between the hull's ends.
+    auto gap = [&](int b, int e) {
+      const uint32_t before = __ballot_sync(kAll, b < e) & ((1u << lane) - 1);
+      const int src = before != 0 ? 31 - __clz(before) : lane;
+      return apart(__shfl_sync(kAll, b, src), __shfl_sync(kAll, e, src), b, e);
+    };
+    const bool gap_v = gap(r.x, r.y), gap_c = gap(r.z, r.w);
+    const int gaps = __any_sync(kAll, gap_v || gap_c);
     if (lane == 0) hull[warp][0] = a, hull[warp][1] = b, hull[warp][2] = c, hull[warp][3] = e;
+    if (lane == 0) hull_gaps[warp] = gaps;
     if (grp == 0) row_ref[row] = -INFINITY;
   }
   if (tid == 0) {
@@ -486,9 +502,41 @@ __global__ void __launch_bounds__(kThreads, 1) attend_dense_kernel(
       // -------------------------------------------------------------------- tile watch
       // Waits for V(t) and K(t + 3) in the MMA warp's stead and arrives at pready for them: a
       // barrier test takes a few hundred cycles while the MMAs read shared memory, and the MMA
-      // warp's are all in the way.
+      // warp's are all in the way.  Zeros the rows of V that no query row sees: those past the
+      // hull that are not past the tensor (those TMA fills with zeros), or all of them where the
+      // ranges have gaps.
+      bool gaps = false;
+      for (int w = 0, v = 0, c = 0; w < 4; ++w) {          // v, c: the last warp with such keys
+        gaps |= hull_gaps[w] || apart(hull[v][0], hull[v][1], hull[w][0], hull[w][1]) ||
+                apart(hull[c][2], hull[c][3], hull[w][2], hull[w][3]);
+        if (hull[w][0] < hull[w][1]) v = w;
+        if (hull[w][2] < hull[w][3]) c = w;
+      }
       for (int t = 0; t < T; ++t) {
-        if (!wait_slot(slot_v(t, T)) || (t + 3 < T && !wait_slot(slot_k(t + 3)))) break;
+        if (!wait_slot(slot_v(t, T))) break;
+        const int y = tl.row(t);
+        const bool video = tl.video(t);
+        const int end = (video ? tl.ve : tl.ce) - y, rows = (video ? nk : nc) - y;
+        if (gaps || (end < 128 && end < rows)) {
+          uint8_t* v = ring + (slot_v(t, T) % kStages) * C::kTile;
+#pragma unroll 1
+          for (int w = 0; w < 4; ++w) {                    // keys y + 32 w .. of the tile
+            uint32_t seen = 0;
+            for (int i = q0 + lane; i < min(q0 + 128, nq); i += 32) {
+              const int4 o = ranges[i];
+              const int key = y + 32 * w;
+              seen |= bits32(max(video ? o.x : o.z, 0) - key, max(video ? o.y : o.w, 0) - key);
+            }
+            seen = __reduce_or_sync(kAll, seen);
+            if (!(seen >> lane & 1))
+              for (int k = 0; k < kAtoms * 8; ++k)
+                *reinterpret_cast<uint4*>(v + (k / 8) * 16384 + (32 * w + lane) * 128 +
+                                          (k % 8) * 16) = make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+        }
+        if (t + 3 < T && !wait_slot(slot_k(t + 3))) break;
         // the phase before has to be over, or this would count for it: S(t) is behind PV(t - 3)
         if (!wait_s(t)) break;
         if (elect_one()) mbar_arrive(&bars.pready[t % 3]);
@@ -586,17 +634,6 @@ __global__ void __launch_bounds__(kThreads, 1) attend_dense_kernel(
 #pragma unroll
       for (int i = 0; i < 4; ++i) tmem_st16_issue(sbuf + 16 * i, pk[i]);
       tmem_wait_st();
-      // V rows past the hull that are not past the tensor (those TMA fills with zeros)
-      const int end = (video ? tl.ve : tl.ce) - y, rows = (video ? nk : nc) - y;
-      if (end < 128 && end < rows) {
-        const int i = slot_v(t, T);
-        if (!(ok = wait_slot(i))) break;
-        uint8_t* v = ring + (i % kStages) * C::kTile;
-        for (int a = 0; a < kAtoms; ++a)
-          for (int k = end * 8 + row; k < 128 * 8; k += 128)
-            *reinterpret_cast<uint4*>(v + a * 16384 + k * 16) = make_uint4(0, 0, 0, 0);
-        fence_proxy_async_smem();
-      }
       tc_fence_before_sync();
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars.pready[t % 3]);

@@ -593,9 +593,10 @@ SPARK_API spark_status spark_rope_frequencies(const int32_t* axis_pairs, int nax
  *     partial sums of calls with few rows, whose keys are split over the GPU and joined by a
  *     second kernel in a fixed order (results are deterministic).  Calls that may overlap on the
  *     GPU need a workspace each.
- *   - Keys of a row's masked places may hold anything, NaN included.  So may a value row that lies
- *     outside the ranges of its query rows' tile (128 rows from a multiple of 128), from the
- *     smallest begin to the largest end in it; elsewhere 0 * NaN reaches the rows that mask it.
+ *   - Keys of a row's masked places may hold anything, NaN included.  So may a value row that no
+ *     row of a tile of 128 query rows (from a multiple of 128) sees.  A value row that some rows of
+ *     the tile see and others mask adds nothing to the latter while it is finite; an infinity or
+ *     NaN in it reaches them, as 0 * NaN.
  *   - bf16 tensor-core products with fp32 sums; probabilities are rounded to bf16. */
 #define SPARK_MAX_DENSE (1 << 30)
 

@@ -206,6 +206,57 @@ def test_masked_values_as_large_as_the_type_holds(d):
     check(odd, out[:, 1::2], lse[:, 1::2], r[1::2].contiguous())
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("order", ["up", "down", "mixed", "holes"])
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+def test_padding_between_the_segments_may_hold_anything(d, order, bad):
+    """Keys in segments with padding between them, several segments to a tile of queries, rows of
+    nothing among them."""
+    nq, nk, nc = 300, 2000, 260
+    x = inputs(18, 2, nq, nk, nc, d)
+    starts = list(range(10, 1900, 190))                    # 10 segments, 30 rows each
+    lens = [150, 190, 1, 127, 128, 129, 64, 100, 33, 180]
+    which = list(range(10))
+    if order == "down":
+        which = which[::-1]
+    if order == "mixed":
+        which = [3, 0, 7, 7, 1, 9, 2, 8, 4, 6]
+    r = torch.zeros(nq, 4, dtype=torch.int32)
+    for i, b in enumerate(which):
+        r[30 * i:30 * i + 30] = torch.tensor([starts[b], starts[b] + lens[b], 26 * b, 26 * b + 20])
+    if order == "holes":
+        r[::3, :2] = 0
+        r[1::3, 2:] = 7
+        r[125:131] = 0
+    used = torch.zeros(nk, dtype=torch.bool), torch.zeros(nc, dtype=torch.bool)
+    for a, b, c, e in r.tolist():
+        used[0][a:b], used[1][c:e] = True, True
+    for t, u in (("K", 0), ("V", 0), ("Kc", 1), ("Vc", 1)):
+        x[t][:, (~used[u]).to(DEV)] = bad
+    r = r.to(DEV)
+    out, lse = spark_attend_dense(**x, ranges=r, out_dtype=torch.float32)
+    for t, u in (("K", 0), ("V", 0), ("Kc", 1), ("Vc", 1)):
+        x[t][:, (~used[u]).to(DEV)] = 0
+    check(x, out, lse, r)
+
+
+def test_range_bounds_of_any_int32():
+    low, high = -2 ** 31, 2 ** 31 - 1
+    x = inputs(19, 2, 5, 900, 300, 128)
+    r = torch.tensor([[low, 20, low, high], [800, high, low, low], [high, low, 100, high],
+                      [low, high, high, high], [high, high, low, 1]], dtype=torch.int32, device=DEV)
+    out, lse = spark_attend_dense(**x, ranges=r, out_dtype=torch.float32)
+    check(x, out, lse, r.clamp(min=0))
+    r = r[:3].contiguous()
+    r[0, 1] = r[1, 3] = r[2, 1] = 20                       # a gap between keys 20 and 800
+    x["Q"] = x["Q"][:, :3].contiguous()
+    x["V"][:, 20:800] = math.nan
+    r[2, 0] = low
+    out, lse = spark_attend_dense(**x, ranges=r, out_dtype=torch.float32)
+    x["V"][:, 20:800] = 0
+    check(x, out, lse, r.clamp(min=0))
+
+
 def test_nan_in_a_live_key_reaches_its_rows_only():
     x = inputs(9, 1, 2, 600, 0, 128)
     x["K"][0, 500] = math.nan
