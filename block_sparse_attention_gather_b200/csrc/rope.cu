@@ -84,6 +84,9 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas)
   const bool live = n < a.N;
   const int h0 = blockIdx.y * heads_per_cta, h1 = min(h0 + heads_per_cta, a.H);
   const float* weight = t < 2 ? a.weight[t] : nullptr;
+  // set up while the kernel before it ends, and so may the one behind it be: no global memory is
+  // touched before the wait (back to back: 16384 tokens 41.5 -> 39.6 us, one token 12.2 -> 11.7)
+  asm volatile("griddepcontrol.launch_dependents;\n\tgriddepcontrol.wait;" ::: "memory");
 
   // Columns of the thread's two vectors.  Half layout: the two sides of V pairs.  Interleaved (and
   // unrotated) rows: one vector in each half of the row with V/2 whole pairs each, so that a
@@ -252,8 +255,16 @@ static cudaError_t launch_rope_t(const RopeArgs& a, cudaStream_t s) {
   const auto kern = V > 1 && a.interleaved && a.pairs % (V > 1 ? V / 2 : 1) != 0
                         ? qk_norm_rope_kernel<T, D, V, C, (V > 1)>
                         : qk_norm_rope_kernel<T, D, V, C, false>;
-  kern<<<dim3(blocks, (a.H + per - 1) / per, tensors), kRopeThreads, 0, s>>>(a, per);
-  return cudaGetLastError();
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(blocks, (a.H + per - 1) / per, tensors);
+  cfg.blockDim = dim3(kRopeThreads);
+  cfg.stream = s;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, a, per);
 }
 
 // The widest access that every row start, stride and half allows.

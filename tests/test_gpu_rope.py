@@ -12,7 +12,7 @@ import math
 import pytest
 import torch
 
-from block_sparse_attention_gather_b200 import (SparkError, spark_qk_norm_rope,
+from block_sparse_attention_gather_b200 import (SparkError, spark_attend_dense, spark_qk_norm_rope,
                                                 spark_rope_frequencies)
 
 pytestmark = pytest.mark.gpu
@@ -152,6 +152,48 @@ def test_every_count_of_pairs_and_what_lies_behind_them(dtype, interleaved, shif
         ones = torch.where(torch.isfinite(x), x, torch.ones_like(x))
         want = reference(ones, None, 1e-6, pos, freq, [pairs], interleaved, 1.0)
         check(got[..., :2 * pairs], [t[..., :2 * pairs] for t in want])
+
+
+@pytest.mark.parametrize("N", [1, 77, 5000])
+@pytest.mark.parametrize("captured", [False, True])
+def test_calls_that_feed_each_other(N, captured):
+    """Each call reads what the one before it wrote and writes what that one read, without a pause;
+    the dense attention between them reads the keys and writes the next queries."""
+    (Q, K, V), g = inputs(N, 4, N, 128, BF, packed=False)
+    w = torch.rand(128, generator=g, device=DEV) + 0.5
+    pos = torch.arange(N, device=DEV, dtype=torch.int32)[:, None]
+    freq = spark_rope_frequencies([64])[0].to(DEV)
+
+    def chain(pause):
+        a, b = [t.clone() for t in (Q, K, V)], [torch.empty_like(t) for t in (Q, K, V)]
+        for i in range(6):
+            spark_qk_norm_rope(*a, w, w, 1e-6, pos, freq, [64], i % 2 == 1, Q_out=b[0], K_out=b[1],
+                               V_out=b[2])
+            pause()
+            if i % 3 == 2:
+                spark_attend_dense(b[0], b[1], b[2], out=a[0])
+                pause()
+                spark_qk_norm_rope(a[0], b[1], b[2], w, w, 1e-6, pos, freq, [64], K_out=a[1],
+                                   Q_out=b[0], V_out=a[2])
+                pause()
+                b[1], a[1] = a[1], b[1]
+                b[2], a[2] = a[2], b[2]
+            a, b = b, a
+        return a
+
+    want = chain(torch.cuda.synchronize)
+    torch.cuda.synchronize()
+    if captured:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            got = chain(lambda: None)
+        for _ in range(2):
+            graph.replay()
+    else:
+        got = chain(lambda: None)
+    torch.cuda.synchronize()
+    for x, y in zip(got, want):
+        assert torch.isfinite(x).all() and torch.equal(x, y)
 
 
 def test_inputs_that_repeat_themselves():
