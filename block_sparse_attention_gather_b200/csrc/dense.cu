@@ -36,7 +36,7 @@
 // 128 exponentials of a row's tile; the others by polynomial) and the rest the latencies of some
 // 700 instructions in order; the MMAs of a tile take 1024 cycles, and reading Q, K, V and writing
 // K, V in shared memory 1280.  24 heads x 30240 x 30240 take 9.05 ms alone (1241 TFLOP/s) and
-// 9.8 to 10.0 ms in a loop at the 1000 W power cap (1126 to 1147 TFLOP/s, 1470 MHz).
+// 9.7 to 10.0 ms in a loop at the 1000 W power cap (1126 to 1163 TFLOP/s, 1470 MHz).
 //
 // The steps, on that case unless named: running maximum, pair of query tiles per CTA 10.9 ms;
 // no maximum per tile 10.3; registers moved to the softmax warps, polynomial 9.7; tile waits in a
