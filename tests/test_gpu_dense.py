@@ -594,3 +594,50 @@ def test_binding_refusals():
                      ((5, q, [1, 2, 3]), {})):
         with pytest.raises((TypeError, ValueError)):
             spark_attend_ranges(*args, **kw)
+
+
+def test_captured_among_copies_and_on_two_streams():
+    """A graph whose calls follow a memset and a copy, and join branches of two streams."""
+    x = inputs(20, 4, 130, 1500, 0, 128)
+    w = torch.rand(128, device=DEV) + 0.5
+    pos = torch.arange(1500, device=DEV, dtype=torch.int32)[:, None]
+    freq = spark_rope_frequencies([64])[0].to(DEV)
+    q, k, k2, v = x["Q"].clone(), torch.empty_like(x["K"]), torch.empty_like(x["K"]), x["V"].clone()
+    r = torch.empty(130, 4, dtype=torch.int32, device=DEV)
+    qo = torch.tensor([0, 50, 130], dtype=torch.int32, device=DEV)
+    ko = torch.tensor([0, 700, 1500], dtype=torch.int32, device=DEV)
+    out = [torch.empty_like(q) for _ in range(3)]
+    side = torch.cuda.Stream()
+
+    def work():
+        main = torch.cuda.current_stream()
+        k.zero_()
+        spark_qk_norm_rope(x["K"], None, None, w, None, 1e-6, pos, freq, [64], Q_out=k)
+        spark_attend_dense(q, k, v, out=out[0])
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            spark_qk_norm_rope(k, None, None, w, None, 1e-6, pos, freq, [64], Q_out=k2)
+            spark_attend_ranges(130, qo, ko, ranges=r)
+            spark_attend_dense(out[0], k2, v, out=out[1])
+        spark_attend_dense(out[0], k, v, out=out[2])
+        main.wait_stream(side)
+        spark_attend_dense(out[1], k2, out[2].repeat(1, 12, 1)[:, :1500].contiguous(), ranges=r,
+                           out=q)
+        k2.copy_(k)
+        spark_attend_dense(q, k2, v, out=out[0])
+
+    start = x["Q"].clone()
+    want = []
+    for _ in range(3):
+        work()
+        torch.cuda.synchronize()
+        want.append([t.clone() for t in (q, *out)])
+    q.copy_(start)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        work()
+    for i in range(3):
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip((q, *out), want[i]):
+            assert torch.isfinite(a).all() and torch.equal(a, b), i
