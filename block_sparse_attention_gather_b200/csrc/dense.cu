@@ -607,8 +607,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_dense_kernel(
             break;
           const float mx = max_tile(sbuf) * c;
           const bool grow = !(mx <= ref);                  // a NaN among the scores too
-          // a score of +inf leaves no number to compare the others with
-          const float next = grow ? (mx < INFINITY ? mx : NAN) : ref;
+          // a score of +inf leaves no number to compare the others with, and a row that met one, or
+          // a NaN, keeps none: its masked tiles (maximum -inf) must not make it a row without keys
+          const float next = grow ? (ref == ref && mx < INFINITY ? mx : NAN) : ref;
           const float f = grow ? ex2_approx(ref - next) : 1.f;
           ref = next;
           l *= f;

@@ -268,6 +268,27 @@ def test_nan_in_a_live_key_reaches_its_rows_only():
     assert ((out[0, 1].double() - ref[0, 1]).abs() <= 2.0 ** -7 * A[0, 1] + 1e-6).all()
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("nk", [256, 4000])
+@pytest.mark.parametrize("where", ["K", "Q", "inf"])
+def test_nan_row_stays_one_past_its_last_key(nk, d, where):
+    """Row 0's keys end a tile (and more) before those of the row beside it, in one slice of the keys
+    and in several: the tiles where it sees nothing must not make it a row without keys."""
+    x = inputs(70, 1, 2, nk, 0, d)
+    if where == "Q":
+        x["Q"][0, 0, 7] = math.nan
+    elif where == "K":
+        x["K"][0, 5] = math.nan
+    else:
+        x["K"][0, 5], x["Q"][0, 0] = math.inf, x["Q"][0, 0].abs() + 0.5
+    r = torch.tensor([[0, 100, 0, 0], [64, nk, 0, 0]], dtype=torch.int32, device=DEV)
+    out, lse = spark_attend_dense(**x, ranges=r, out_dtype=torch.float32)
+    assert torch.isnan(out[0, 0]).all() and torch.isnan(lse[0, 0])
+    x["K"][0, 5] = 0
+    other = dict(x, Q=x["Q"][:, 1:].contiguous())
+    check(other, out[:, 1:], lse[:, 1:], r[1:].contiguous())
+
+
 @pytest.mark.parametrize("nats", [20, 60, 88, 100, 150, 200])
 @pytest.mark.parametrize("tile", [0, 1, 4])
 @pytest.mark.parametrize("far", [1, -1])
