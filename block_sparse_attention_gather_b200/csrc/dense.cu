@@ -9,10 +9,13 @@
 // One pass over the keys with a running reference per row (an online softmax):
 //   p_j = 2^(s_j log2e - ref),  l = sum p,  O = sum p v,  out = O / l,  lse = (ref + log2 l) ln2.
 // ref is the row's maximum over the first two tiles (the first with a live key).  It is raised to
-// a later tile's maximum, and O and l rescaled, only when that tile's sum of p reaches 2^24 (or is
+// a later tile's maximum, and O and l rescaled, only when that tile's sum of p reaches 2^8 (or is
 // no number): up to there p, rounded to bf16 for the tensor cores, and the fp32 sums keep their
 // relative accuracy, so a reference below the true maximum costs none, and the usual tile needs
 // no maximum at all.  The scores stay in TMEM until the sum is known, so the tile can be redone.
+// A reference at the maximum bounds a tile's sum by 2^7, so large values overflow O at most one
+// power of two earlier than they would there.  (A limit of 2^24 overflowed for values of 2^104 on;
+// its times are the same but for packed prompts, 32.0 us against 32.7.)
 //
 // One CTA works on one head, one 128-row query tile and one slice of the key tiles.  12 warps:
 // 0-3 / 4-7 the softmax groups, which take the even and the odd key tiles (warp w owns TMEM lanes
@@ -67,7 +70,7 @@ static_assert(2 * kRegsSoftmax + kRegsOther == 3 * kRegsLaunch, "register split"
 constexpr uint32_t kColO = 384;              // S/P buffers at TMEM columns 0, 128, 256
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kMaxSum = 0x1p24f;           // a tile's sum of p from which the reference is raised
+constexpr float kMaxSum = 0x1p8f;            // a tile's sum of p from which the reference is raised
 constexpr int kMaxSplits = 64;
 constexpr int kPolyEvery = 3;                // every third pair of exponentials by polynomial
 
@@ -235,7 +238,7 @@ __device__ __forceinline__ uint64_t exp32(const uint32_t (&r)[32], uint64_t c2, 
 }
 
 // The tile's 128 scores at `sbuf` -> packed pairs, returning the sum of p, which is no number
-// under 2^24 when a score is NaN or its p reaches that.  The load of the second half's columns is
+// under 2^8 when a score is NaN or its p reaches that.  The load of the second half's columns is
 // in flight while the first half's are exponentiated.
 __device__ __forceinline__ float exp_tile(uint32_t sbuf, float c, float m, uint32_t (&pk)[4][16]) {
   float top = -INFINITY;

@@ -289,6 +289,28 @@ def test_nan_row_stays_one_past_its_last_key(nk, d, where):
     check(other, out[:, 1:], lse[:, 1:], r[1:].contiguous())
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("nk", [700, 9000])
+@pytest.mark.parametrize("step", [8.0, 14.0, 16.0, 60.0])
+def test_large_values_under_scores_that_rise(nk, d, step):
+    """Values of 2^118 and scores `step` nats higher (14: 20 powers of two) from key 300 on, and again
+    from key 500 on.  The definition is finite, and so is an fp32 sum of p |v| with p <= 1:
+    |v| < 2^118 * 8, and no 2^14 keys make it 2^128 unless they all have p near 1.  A score is one
+    product, exact but for its scale: 2^-22 of 121 is under 2^-15."""
+    g = torch.Generator(device=DEV).manual_seed(71)
+    level = torch.zeros(nk, device=DEV)
+    level[300:] += step
+    level[500:] += step
+    level = level + 0.3 * torch.randn(2, nk, generator=g, device=DEV)
+    Q, K = torch.zeros(2, 40, d, device=DEV), torch.zeros(2, nk, d, device=DEV)
+    Q[..., 0] = 16
+    K[..., 0] = level * math.sqrt(d) / 16
+    V = torch.randn(2, nk, d, generator=g, device=DEV).clamp(-8, 8) * 2.0 ** 118
+    x = dict(Q=Q.to(BF), K=K.to(BF), V=V.to(BF), Kc=None, Vc=None)
+    out, lse = spark_attend_dense(**x, out_dtype=torch.float32)
+    check(x, out, lse)
+
+
 @pytest.mark.parametrize("nats", [20, 60, 88, 100, 150, 200])
 @pytest.mark.parametrize("tile", [0, 1, 4])
 @pytest.mark.parametrize("far", [1, -1])
