@@ -893,6 +893,18 @@ def _stream_of(index, stream):
     return stream.cuda_stream
 
 
+def _empty(shape, dtype, device, stream):
+    """torch.empty for a call on `stream`, from that stream's pool: memory of the current stream's
+    could still be in use there, or be handed out again, while the call works on it.  The current
+    stream is where the caller reads and drops it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream(device))
+    return t
+
+
 def _refuse(t, name, dtype, device, shape):
     """Raises what is wrong with a tensor that failed its check."""
     _need(t, name, dtype, device)
@@ -961,7 +973,7 @@ def spark_qk_norm_rope(Q, K=None, V=None, q_weight=None, k_weight=None, eps=1e-6
         if inner != 1:
             _refuse_rows(Q, "Q", dt, Q.device)
         if Q_out is None:
-            Q_out = torch.empty(shape, dtype=dt, device=Q.device)
+            Q_out = _empty(shape, dt, Q.device, stream)
         if not (Q_out.dtype is dt and Q_out.get_device() == index and Q_out.is_contiguous()
                 and Q_out.shape == shape):
             _refuse(Q_out, "Q_out", dt, Q.device, "[H, N, d] of Q")
@@ -972,7 +984,7 @@ def spark_qk_norm_rope(Q, K=None, V=None, q_weight=None, k_weight=None, eps=1e-6
             if inner != 1 or not (K.dtype is dt and K.get_device() == index and K.shape == shape):
                 _refuse_rows(K, "K", dt, Q.device)
             if K_out is None:
-                K_out = torch.empty(shape, dtype=dt, device=Q.device)
+                K_out = _empty(shape, dt, Q.device, stream)
             if not (K_out.dtype is dt and K_out.get_device() == index and K_out.is_contiguous()
                     and K_out.shape == shape):
                 _refuse(K_out, "K_out", dt, Q.device, "[H, N, d] of Q")
@@ -984,7 +996,7 @@ def spark_qk_norm_rope(Q, K=None, V=None, q_weight=None, k_weight=None, eps=1e-6
             if inner != 1 or not (V.dtype is dt and V.get_device() == index and V.shape == shape):
                 _refuse_rows(V, "V", dt, Q.device)
             if V_out is None:
-                V_out = torch.empty(shape, dtype=dt, device=Q.device)
+                V_out = _empty(shape, dt, Q.device, stream)
             if not (V_out.dtype is dt and V_out.get_device() == index and V_out.is_contiguous()
                     and V_out.shape == shape):
                 _refuse(V_out, "V_out", dt, Q.device, "[H, N, d] of Q")
@@ -1065,7 +1077,7 @@ def spark_attend_ranges(nq, q_offsets, k_offsets=None, c_offsets=None, prefix=No
                 _refuse(prefix, "prefix", i32, q_offsets.device, f"[{n - 1}]")
             p = prefix.data_ptr()
         if ranges is None:
-            ranges = torch.empty(max(int(nq), 0), 4, dtype=i32, device=q_offsets.device)
+            ranges = _empty((max(int(nq), 0), 4), i32, q_offsets.device, stream)
         if not (ranges.dtype is i32 and ranges.get_device() == index and ranges.is_contiguous()
                 and ranges.shape == (nq, 4)):
             _refuse(ranges, "ranges", i32, q_offsets.device, "[nq, 4]")
@@ -1123,18 +1135,18 @@ def spark_attend_dense(Q, K, V, Kc=None, Vc=None, ranges=None, out_dtype=torch.b
                 _refuse(ranges, "ranges", i32, Q.device, "[nq, 4]")
             rg = ranges.data_ptr()
         if out is None:
-            out = torch.empty(shape, dtype=out_dtype, device=Q.device)
+            out = _empty(shape, out_dtype, Q.device, stream)
         code = _code(out.dtype)
         if not (out.get_device() == index and out.is_contiguous() and out.shape == shape):
             _refuse(out, "out", out.dtype, Q.device, "[H, nq, d] of Q")
         if lse is None:
-            lse = torch.empty(H, nq, dtype=f32, device=Q.device)
+            lse = _empty((H, nq), f32, Q.device, stream)
         if not (lse.dtype is f32 and lse.get_device() == index and lse.is_contiguous()
                 and lse.shape == (H, nq)):
             _refuse(lse, "lse", f32, Q.device, "[H, nq]")
         if workspace is None:
-            workspace = torch.empty(spark_attend_dense_workspace_size(H, nq, nk, nc, d),
-                                    dtype=torch.uint8, device=Q.device)
+            workspace = _empty(spark_attend_dense_workspace_size(H, nq, nk, nc, d), torch.uint8,
+                               Q.device, stream)
         if not (workspace.dtype is torch.uint8 and workspace.get_device() == index
                 and workspace.is_contiguous()):
             _need(workspace, "workspace", torch.uint8, Q.device)
@@ -1182,16 +1194,16 @@ def spark_bsa_forward_joint(Q, K, V, Qc, Kc, Vc, q_perm, k_perm, q_offsets, k_of
     nqb, nkb = q_offsets.numel() - 1, k_offsets.numel() - 1
     layout = spark_bsa_workspace_layout(H, N, d, nqb, nkb, topk_ratio)
     if out is None:
-        out = torch.empty_like(Q)
+        out = _empty(Q.shape, Q.dtype, dev, stream)
     if out_c is None:
-        out_c = torch.empty_like(Qc)
+        out_c = _empty(Qc.shape, Q.dtype, dev, stream)
     _need(out, "out", Q.dtype, dev)
     _need(out_c, "out_c", Q.dtype, dev)
     if out.shape != Q.shape or out_c.shape != Qc.shape:
         raise ValueError("out and out_c must have the shapes of Q and Qc")
     if workspace is None:
         size = spark_bsa_workspace_size_joint(H, N, d, nqb, nkb, topk_ratio, nc)
-        workspace = torch.empty(size, dtype=torch.uint8, device=dev)
+        workspace = _empty(size, torch.uint8, dev, stream)
     _need(workspace, "workspace", torch.uint8, dev)
     st = _launch(dev.index, lib().spark_bsa_forward_joint, _ptr(Q), _ptr(K), _ptr(V), _ptr(Qc),
                  _ptr(Kc), _ptr(Vc), nc, _code(Q.dtype), H, N, d, _ptr(q_perm), _ptr(k_perm),

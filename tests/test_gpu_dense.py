@@ -454,6 +454,49 @@ def test_two_streams_at_once():
         assert all(torch.equal(o, w[0]) and torch.equal(l, w[1]) for o, l in g)
 
 
+def test_calls_on_given_streams_without_workspaces():
+    """stream= alone: the calls' own workspaces and outputs are nobody else's while they run, however
+    long they wait for their streams."""
+    xs = [inputs(50 + i, 2, 9, 9000, 33, 128) for i in range(2)]
+    want = [spark_attend_dense(**x) for x in xs]
+    size = spark_attend_dense_workspace_size(2, 9, 9000, 33, 128)
+    assert size > 256                                      # split: partial sums go through it
+    streams = [torch.cuda.Stream() for _ in xs]
+    for _ in range(3):
+        torch.cuda.synchronize()
+        for s in streams:
+            with torch.cuda.stream(s):
+                torch.cuda._sleep(10_000_000)              # a few milliseconds
+        got = [spark_attend_dense(**x, stream=s) for x, s in zip(xs, streams)]
+        other = [torch.full((n,), 255, dtype=torch.uint8, device=DEV)
+                 for n in 2 * [size, want[0][0].nbytes, want[0][1].nbytes]]
+        torch.cuda.synchronize()
+        for g, w in zip(got, want):
+            assert torch.equal(g[0], w[0]) and torch.equal(g[1], w[1])
+        assert all((t == 255).all() for t in other)
+
+
+def test_captured_calls_on_given_streams_without_workspaces():
+    xs = [inputs(52 + i, 2, 9, 9000, 33, 128) for i in range(2)]
+    want = [spark_attend_dense(**x) for x in xs]
+    streams = [torch.cuda.Stream() for _ in xs]
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        main = torch.cuda.current_stream()
+        for s in streams:
+            s.wait_stream(main)
+        got = [spark_attend_dense(**x, stream=s) for x, s in zip(xs, streams)]
+        for s in streams:
+            main.wait_stream(s)
+        copies = [[t.clone() for t in g] for g in got]
+    for _ in range(3):
+        graph.replay()
+    torch.cuda.synchronize()
+    for g, w in zip(copies, want):
+        assert torch.equal(g[0], w[0]) and torch.equal(g[1], w[1])
+
+
 @pytest.mark.parametrize("H,nq,nk", [(2, 7, 9000), (8, 300, 300), (1, 128, 128)])
 def test_calls_that_feed_each_other(H, nq, nk):
     """Each call's output is the next one's queries, in the same buffers: kernels may be set up
