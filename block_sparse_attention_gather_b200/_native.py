@@ -202,6 +202,18 @@ def _check(fn, status):
         raise SparkError(fn, status)
 
 
+def _empty(shape, dtype, device, stream):
+    """torch.empty for a call on `stream`, from that stream's pool: memory of the current stream's
+    could still be in use there, or be handed out again, while the call works on it.  The current
+    stream is where the caller reads and drops it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream(device))
+    return t
+
+
 # ------------------------------------------------------------------------- host calls
 
 def spark_status_string(status: int) -> str:
@@ -764,11 +776,11 @@ def spark_reblock(Q, K, block, mode="q_reuse_k", workspace=None, stream=None):
         raise ValueError("Q and K must share the shape [H, N, d]")
     layout = spark_reblock_workspace_layout(H, N, d, block)
     if workspace is None:
-        workspace = torch.empty(layout.total, dtype=torch.uint8, device=Q.device)
+        workspace = _empty(layout.total, torch.uint8, Q.device, stream)
     _need(workspace, "workspace", torch.uint8, Q.device)
-    q_perm = torch.empty(H, N, dtype=torch.int32, device=Q.device)
-    k_perm = torch.empty_like(q_perm)
-    offsets = torch.empty(layout.nb + 1, dtype=torch.int32, device=Q.device)
+    q_perm = _empty((H, N), torch.int32, Q.device, stream)
+    k_perm = _empty((H, N), torch.int32, Q.device, stream)
+    offsets = _empty(layout.nb + 1, torch.int32, Q.device, stream)
     st = lib().spark_reblock(_ptr(Q), _ptr(K), _code(Q.dtype), H, N, d, int(block),
                              REBLOCK_MODES[mode], _ptr(q_perm), _ptr(k_perm), _ptr(offsets),
                              _ptr(workspace), workspace.numel(), _stream(stream))
@@ -853,15 +865,15 @@ def spark_bsa_forward_host(Q, K, V, q_perm, k_perm, q_offsets, k_offsets, topk_r
     if out is None:
         out = torch.empty_like(Q).pin_memory()
     _need_host(out, "out", Q.dtype)
-    if staging is None:
-        staging = torch.empty(spark_bsa_host_staging_size_ex(H, N, d, Q.dtype, nqb, nkb, hpc, nc),
-                              dtype=torch.uint8, device=dev)
+    if streams is None:
+        streams = (torch.cuda.current_stream(dev), torch.cuda.Stream(dev), torch.cuda.Stream(dev))
+    if staging is None:                  # the copy streams start and end within the compute stream
+        staging = _empty(spark_bsa_host_staging_size_ex(H, N, d, Q.dtype, nqb, nkb, hpc, nc),
+                         torch.uint8, dev, streams[0])
     if workspace is None:
         size = (spark_bsa_workspace_size_fp8(hpc, N, d, nqb, nkb, topk_ratio, nc) if fp8 else
                 spark_bsa_workspace_size_ctx(hpc, N, d, nqb, nkb, topk_ratio, nc))
-        workspace = torch.empty(size, dtype=torch.uint8, device=dev)
-    if streams is None:
-        streams = (torch.cuda.current_stream(dev), torch.cuda.Stream(dev), torch.cuda.Stream(dev))
+        workspace = _empty(size, torch.uint8, dev, streams[0])
     sc, sh, sd = (ctypes.c_void_p(s.cuda_stream) for s in streams)
     st = lib().spark_bsa_forward_host_ex(_ptr(Q), _ptr(K), _ptr(V),
                                          _ptr(Kc) if nc else None, _ptr(Vc) if nc else None, nc,
@@ -891,18 +903,6 @@ def _stream_of(index, stream):
     if stream is None:
         return torch._C._cuda_getCurrentRawStream(index)
     return stream.cuda_stream
-
-
-def _empty(shape, dtype, device, stream):
-    """torch.empty for a call on `stream`, from that stream's pool: memory of the current stream's
-    could still be in use there, or be handed out again, while the call works on it.  The current
-    stream is where the caller reads and drops it."""
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    with torch.cuda.stream(stream):
-        t = torch.empty(shape, dtype=dtype, device=device)
-    t.record_stream(torch.cuda.current_stream(device))
-    return t
 
 
 def _refuse(t, name, dtype, device, shape):

@@ -89,12 +89,20 @@ def perms(n):
     return p, p, ints(0, n), ints(0, n)
 
 
+def host(n):
+    x, p, o = torch.zeros(2, n, 128, dtype=BF), torch.zeros(2, n, dtype=I32), torch.tensor([0, n])
+    return x, x, x, p, p, o.int(), o.int()
+
+
 CALLS = {
     "attend_dense": (3, lambda s: bsa.spark_attend_dense(rows(5), rows(9), rows(9), stream=s)),
     "qk_norm_rope": (3, lambda s: bsa.spark_qk_norm_rope(rows(5), rows(5), rows(5), stream=s)),
     "attend_ranges": (1, lambda s: bsa.spark_attend_ranges(5, ints(0, 5), stream=s)),
     "forward_joint": (3, lambda s: bsa.spark_bsa_forward_joint(
         rows(9), rows(9), rows(9), rows(4), rows(4), rows(4), *perms(9), 0.5, stream=s)),
+    "reblock": (4, lambda s: bsa.spark_reblock(rows(9), rows(9), 4, stream=s)),
+    "forward_host": (2, lambda s: bsa.spark_bsa_forward_host(
+        *host(9), 0.5, out=host(9)[0], streams=(s, MAIN, MAIN))),
 }
 
 

@@ -62,3 +62,21 @@ def test_host_pipeline_fp8_equals_device_forward(hpc, nc):
                                  Vc=Vc.cpu().pin_memory() if nc else None)
     torch.cuda.synchronize()
     assert torch.equal(out, ref.cpu())
+
+
+def test_host_pipeline_on_given_streams_without_staging():
+    """The call's own staging and workspace are nobody else's while its streams wait and run."""
+    x = custom_inputs(104, H=4, N=2000, d=128, dtype="bf16", lo=20, hi=128)
+    host = {n: x[n].cpu().pin_memory() for n in x}
+    args = [host[n] for n in ("Q", "K", "V", "q_perm", "k_perm", "q_offsets", "k_offsets")]
+    want = spark_bsa_forward_host(*args, 0.15)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    with torch.cuda.stream(streams[0]):
+        torch.cuda._sleep(10_000_000)                       # a few milliseconds
+    got = spark_bsa_forward_host(*args, 0.15, streams=streams)
+    other = [torch.full((n,), 255, dtype=torch.uint8, device="cuda")
+             for n in (1 << 20, 1 << 22, 1 << 23, 1 << 24, 1 << 25)]
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
+    assert all((t == 255).all() for t in other)

@@ -230,3 +230,22 @@ def test_reblock_then_forward():
                                                                 hh["k_offsets"], r.sel[A])
                                       for A in range(0, len(o) - 1, 16)]))
     assert np.mean(rec["reblock"]) > np.mean(rec["random"]), rec
+
+
+def test_on_a_given_stream_without_a_workspace():
+    """The call's own workspace is nobody else's while it waits and runs on its stream."""
+    from block_sparse_attention_gather_b200 import spark_reblock_workspace_layout
+    g = torch.Generator(device="cuda").manual_seed(11)
+    Q, K = (torch.randn(3, 2000, 128, generator=g, device="cuda").bfloat16() for _ in range(2))
+    size = spark_reblock_workspace_layout(3, 2000, 128, 128).total
+    want = spark_reblock(Q, K, 128)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(10_000_000)                       # a few milliseconds
+    got = spark_reblock(Q, K, 128, stream=side)
+    other = [torch.full((n,), 255, dtype=torch.uint8, device="cuda")
+             for n in (size, *(t.nbytes for t in want))]
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert all((t == 255).all() for t in other)
