@@ -74,6 +74,12 @@ size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
+// Whether [a, a + na) and [b, b + nb) share a byte.
+bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return na > 0 && nb > 0 && (x < y ? y - x < na : x - y < nb);
+}
+
 cudaStream_t as_stream(void* s) { return static_cast<cudaStream_t>(s); }
 
 int topk_count(int nkb, double ratio) {
@@ -1164,6 +1170,13 @@ spark_status spark_bsa_forward_joint(const void* Q, const void* K, const void* V
   if (!workspace || !aligned(workspace, kAlign) ||
       workspace_bytes < base + cbytes + attend_dense_workspace(H, nc, N, nc, d))
     return SPARK_ERR_WORKSPACE;
+  // the context rows are read by both passes, after and while the outputs are written
+  const size_t row_bytes = static_cast<size_t>(H) * d * (dtype == SPARK_F32 ? 4 : 2);
+  const size_t nbytes = row_bytes * N, ncbytes = row_bytes * nc;
+  for (const void* in : {Qc, Kc, Vc})
+    if (overlap(out_c, ncbytes, in, ncbytes) || overlap(out, nbytes, in, ncbytes))
+      return SPARK_ERR_INVALID_ARG;
+  if (overlap(out, nbytes, out_c, ncbytes)) return SPARK_ERR_INVALID_ARG;
   cudaStream_t s = as_stream(stream);
   st = forward_impl(Q, K, V, Kc, Vc, nc, dtype, H, N, d, q_perm, k_perm, q_block_offsets, nqb,
                     k_block_offsets, nkb, topk_ratio, out, workspace, base, s);

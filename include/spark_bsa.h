@@ -630,8 +630,9 @@ SPARK_API spark_status spark_attend_ranges(int nq, int nseg, const int32_t* q_of
 /* The attention of a block whose context tokens are queries too: spark_bsa_forward_ctx for the
  * video queries, then spark_attend_dense for the context queries Qc [H,nc,d] over every video
  * and context key, with their output in out_c [H,nc,d] (both of `dtype`).  nc >= 1.  The keys of
- * the dense part are the workspace's reblocked ones (their order does not matter).  workspace:
- * spark_bsa_workspace_size_joint bytes, starting with spark_bsa_forward_ctx's. */
+ * the dense part are the workspace's reblocked ones (their order does not matter).  Neither output
+ * may overlap Qc, Kc, Vc or the other (refused).  workspace: spark_bsa_workspace_size_joint bytes,
+ * starting with spark_bsa_forward_ctx's. */
 SPARK_API size_t spark_bsa_workspace_size_joint(int H, int N, int d, int nqb, int nkb,
                                                 double topk_ratio, int nc);
 

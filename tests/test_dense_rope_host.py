@@ -195,6 +195,32 @@ def test_joint_sizes_and_refusals(L):
     assert joint(dtype=5, ws_bytes=1 << 40) == INVALID
 
 
+def test_joint_outputs_over_inputs_are_refused(L):
+    """By their bytes, not their first byte alone; what only touches is none of it.  A call that is
+    not refused ends at the launch, as there is no GPU."""
+    at = ctypes.c_void_p
+    n, c = 2 * 1000 * 128 * 2, 2 * 77 * 128 * 2              # bytes of Q, K, V and of the context's
+
+    def joint(**kw):
+        v = dict(Q=at(0x1000000), K=at(0x2000000), V=at(0x3000000), Qc=at(0x4000000),
+                 Kc=at(0x5000000), Vc=at(0x6000000), nc=77, dtype=0, H=2, N=1000, d=128, qp=P, kp=P,
+                 qo=P, nqb=10, ko=P, nkb=10, ratio=0.2, out=at(0x7000000), out_c=at(0x8000000),
+                 ws=at(0x9000000), ws_bytes=1 << 30, stream=None)
+        v.update(kw)
+        return L.spark_bsa_forward_joint(*v.values())
+
+    if not torch.cuda.is_available():
+        assert joint() not in (OK, INVALID)
+        assert joint(out_c=at(0x4000000 - c), out=at(0x4000000 + c)) not in (OK, INVALID)
+    for start in (0x4000000, 0x5000000, 0x6000000):
+        for shift in (0, c - 16, 16 - c):
+            assert joint(out_c=at(start + shift)) == INVALID
+        for shift in (0, c - 16, 16 - n):
+            assert joint(out=at(start + shift)) == INVALID
+    for shift in (0, n - 16, 16 - c):
+        assert joint(out_c=at(0x7000000 + shift)) == INVALID
+
+
 def test_binding_refuses_host_tensors_and_types():
     t = torch.zeros(1, 8, 128, dtype=torch.bfloat16)
     with pytest.raises(ValueError, match="CUDA tensor"):
