@@ -5,6 +5,7 @@
 #include <atomic>
 #include <cmath>
 #include <cstring>
+#include <utility>
 
 #include "../../include/spark_bsa.h"
 #include "spark_kernels.cuh"
@@ -1124,11 +1125,20 @@ spark_status spark_attend_dense(const void* Q, const void* K, const void* V, con
       (nk > 0 && (!aligned(K, 16) || !aligned(V, 16))) ||
       (nc > 0 && (!aligned(Kc, 16) || !aligned(Vc, 16))))
     return SPARK_ERR_INVALID_ARG;
-  if (out == Q || (nk > 0 && (out == K || out == V)) || (nc > 0 && (out == Kc || out == Vc)))
-    return SPARK_ERR_INVALID_ARG;
+  const size_t row = static_cast<size_t>(H) * d * 2;
+  const size_t out_bytes = row * nq * (out_dtype == SPARK_F32 ? 2 : 1);
+  const std::pair<const void*, size_t> in[] = {
+      {Q, row * nq}, {K, row * nk}, {V, row * nk}, {Kc, row * nc}, {Vc, row * nc},
+      {ranges, ranges ? 16 * static_cast<size_t>(nq) : 0}};
+  for (const auto& t : in)
+    if (overlap(out, out_bytes, t.first, t.second)) return SPARK_ERR_INVALID_ARG;
   if (!workspace || workspace_bytes < attend_dense_workspace(H, nq, nk, nc, d) ||
       !aligned(workspace, kAlign))
     return SPARK_ERR_WORKSPACE;
+  const size_t lse_bytes = lse ? static_cast<size_t>(H) * nq * 4 : 0;
+  for (const auto& t : in)
+    if (overlap(lse, lse_bytes, t.first, t.second)) return SPARK_ERR_INVALID_ARG;
+  if (overlap(lse, lse_bytes, out, out_bytes)) return SPARK_ERR_INVALID_ARG;
   return dense_impl(Q, K, V, Kc, Vc, H, nq, nk, nc, d, ranges, out, out_dtype, lse, workspace, err,
                     as_stream(stream));
 }

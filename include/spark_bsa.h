@@ -588,7 +588,8 @@ SPARK_API spark_status spark_rope_frequencies(const int32_t* axis_pairs, int nax
  *   - ranges: device int32 [nq,4], 16-byte aligned, shared by all heads: {r0, r1, r2, r3} per row,
  *     cut to [0,nk) and [0,nc) (r1 <= r0: none of the video keys).  NULL: every row attends all.
  *     spark_attend_ranges builds those of packed segments.
- *   - out: [H,nq,d] of out_dtype; lse: fp32 [H,nq], may be NULL.  Neither may overlap an input.
+ *   - out: [H,nq,d] of out_dtype; lse: fp32 [H,nq], may be NULL.  Neither may overlap an input or
+ *     the other (refused).
  *   - workspace: device, 256-byte aligned, spark_attend_dense_workspace_size bytes (never 0): the
  *     partial sums of calls with few rows, whose keys are split over the GPU and joined by a
  *     second kernel in a fixed order (results are deterministic).  Calls that may overlap on the

@@ -221,6 +221,30 @@ def test_joint_outputs_over_inputs_are_refused(L):
         assert joint(out_c=at(0x7000000 + shift)) == INVALID
 
 
+def test_dense_outputs_over_inputs_are_refused(L):
+    """As above."""
+    at = ctypes.c_void_p
+    nq, nk, nc = (2 * r * 128 * 2 for r in (300, 1000, 10))
+
+    def attend(**kw):
+        v = dict(Q=at(0x1000000), K=at(0x2000000), V=at(0x3000000), Kc=at(0x5000000),
+                 Vc=at(0x6000000), lse=at(0x7000000), out=at(0x8000000), ws=at(0x9000000),
+                 ws_bytes=1 << 30, ranges=at(0xa000000))
+        return dense(L, **{**v, **kw})
+
+    if not torch.cuda.is_available():
+        assert attend() not in (OK, INVALID)
+        assert attend(out=at(0x1000000 + nq), lse=at(0x2000000 + nk)) not in (OK, INVALID)
+    for start, size in ((0x1000000, nq), (0x2000000, nk), (0x3000000, nk), (0x5000000, nc),
+                        (0x6000000, nc), (0xa000000, 300 * 16)):
+        for shift in (0, size - 16, 16 - nq):
+            assert attend(out=at(start + shift)) == INVALID
+        assert attend(lse=at(start + size - 4)) == INVALID
+        assert attend(lse=at(start + 4 - 2 * 300 * 4)) == INVALID
+    assert attend(lse=at(0x8000000 + nq - 4)) == INVALID
+    assert attend(out_dtype=1, out=at(0x1000000 - 2 * nq + 16)) == INVALID
+
+
 def test_binding_refuses_host_tensors_and_types():
     t = torch.zeros(1, 8, 128, dtype=torch.bfloat16)
     with pytest.raises(ValueError, match="CUDA tensor"):
