@@ -947,11 +947,12 @@ _AXES = {}                       # axis counts -> (their sum, the array the libr
 
 def _axes(axis_pairs):
     key = tuple(axis_pairs)
-    if key not in _AXES:
+    made = _AXES.get(key)
+    if made is None:                 # one look: another thread may empty the table at any point
         if len(_AXES) > 256:
             _AXES.clear()
-        _AXES[key] = (sum(key), (ctypes.c_int32 * len(key))(*key))
-    return _AXES[key]
+        made = _AXES[key] = (sum(key), (ctypes.c_int32 * len(key))(*key))
+    return made
 
 
 def spark_qk_norm_rope(Q, K=None, V=None, q_weight=None, k_weight=None, eps=1e-6, positions=None,

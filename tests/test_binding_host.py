@@ -49,3 +49,24 @@ def test_step_wrappers_refuse_host_tensors():
     sel = torch.zeros(1, 2, 1, dtype=torch.int32)
     with pytest.raises(ValueError, match="CUDA tensor"):
         spark_bsa_attend_var(Q, Q, Q, Q, Q, f, sel, sel[..., 0], perm, offs, offs)
+
+
+def test_axis_counts_survive_another_thread_that_empties_the_table(monkeypatch):
+    """The table of converted axis counts may be emptied between any two of a call's steps."""
+    from block_sparse_attention_gather_b200 import _native
+
+    class Emptied(dict):
+        def __setitem__(self, key, value):
+            super().__setitem__(key, value)
+            self.clear()
+
+        def __contains__(self, key):
+            found = super().__contains__(key)
+            self.clear()
+            return found
+
+    monkeypatch.setattr(_native, "_AXES", Emptied())
+    for filled in ({}, {(16, 24): (40, None)}):
+        dict.update(_native._AXES, filled)
+        total, counts = _native._axes([16, 24])
+        assert total == 40 and (filled or list(counts) == [16, 24])
