@@ -905,7 +905,7 @@ __global__ void __launch_bounds__(256) attend_ranges_kernel(
   // the last b with q_offsets[b] <= i
   int lo = 0, hi = nseg + 1;
   while (lo < hi) {
-    const int mid = (lo + hi) / 2;
+    const int mid = lo + (hi - lo) / 2;        // lo + hi passes 2^31 at 2^30 segments
     if (q_offsets[mid] <= i) lo = mid + 1; else hi = mid;
   }
   const int b = lo - 1;

@@ -571,6 +571,15 @@ def test_ranges_of_segments(nseg, rows, pad, causal):
         assert np.array_equal(got.cpu().numpy(), want)
 
 
+def test_ranges_of_the_most_segments():
+    """2^30 segments, empty but for the first and the last: the search's bounds add up to 2^31."""
+    n = 1 << 30
+    q = torch.full((n + 1,), 2, dtype=torch.int32, device=DEV)          # 4.3 GB
+    q[0], q[-1] = 0, 5
+    got = spark_attend_ranges(7, q, None, q)
+    assert got.tolist() == [[0, 0, 0, 2]] * 2 + [[0, 0, 2, 5]] * 3 + [[0, 0, 0, 0]] * 2
+
+
 def test_ranges_refuse_decreasing_key_offsets_in_the_error_word():
     q = torch.tensor([0, 2, 4], dtype=torch.int32, device=DEV)
     k = torch.tensor([0, 9, 5], dtype=torch.int32, device=DEV)
