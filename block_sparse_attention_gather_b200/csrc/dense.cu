@@ -14,8 +14,11 @@
 // relative accuracy, so a reference below the true maximum costs none, and the usual tile needs
 // no maximum at all.  The scores stay in TMEM until the sum is known, so the tile can be redone.
 // A reference at the maximum bounds a tile's sum by 2^7, so large values overflow O at most one
-// power of two earlier than they would there.  (A limit of 2^24 overflowed for values of 2^104 on;
-// its times are the same but for packed prompts, 32.0 us against 32.7.)
+// power of two earlier than they would there (a limit of 2^24 did so from 2^104 on).  A raised
+// reference goes 2^16 beyond the maximum, as scores that rose once tend to rise again: 8 heads x 8192
+// x 8192 with scores that rise by 25 nats over the keys take 280 us, 418 if it went to the maximum
+// (by 100 nats: 286 and 461; 264 and 277 with the limit of 2^24).  What that costs is the lower end:
+// in such rows values under 2^-110 have products below fp32's normal numbers.
 //
 // One CTA works on one head, one 128-row query tile and one slice of the key tiles.  12 warps:
 // 0-3 / 4-7 the softmax groups, which take the even and the odd key tiles (warp w owns TMEM lanes
@@ -71,6 +74,7 @@ constexpr uint32_t kColO = 384;              // S/P buffers at TMEM columns 0, 1
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kMaxSum = 0x1p8f;            // a tile's sum of p from which the reference is raised
+constexpr float kRoom = 16.f;                // powers of two a raised reference is put above the maximum
 constexpr int kMaxSplits = 64;
 constexpr int kPolyEvery = 3;                // every third pair of exponentials by polynomial
 
@@ -612,7 +616,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_dense_kernel(
           const bool grow = !(mx <= ref);                  // a NaN among the scores too
           // a score of +inf leaves no number to compare the others with, and a row that met one, or
           // a NaN, keeps none: its masked tiles (maximum -inf) must not make it a row without keys
-          const float next = grow ? (ref == ref && mx < INFINITY ? mx : NAN) : ref;
+          const float room = ref == -INFINITY ? 0.f : kRoom;
+          const float next = grow ? (ref == ref && mx < INFINITY ? mx + room : NAN) : ref;
           const float f = grow ? ex2_approx(ref - next) : 1.f;
           ref = next;
           l *= f;
