@@ -15,10 +15,10 @@
 // no maximum at all.  The scores stay in TMEM until the sum is known, so the tile can be redone.
 // A reference at the maximum bounds a tile's sum by 2^7, so large values overflow O at most one
 // power of two earlier than they would there (a limit of 2^24 did so from 2^104 on).  A raised
-// reference goes 2^16 beyond the maximum, as scores that rose once tend to rise again: 8 heads x 8192
-// x 8192 with scores that rise by 25 nats over the keys take 280 us, 418 if it went to the maximum
-// (by 100 nats: 286 and 461; 264 and 277 with the limit of 2^24).  What that costs is the lower end:
-// in such rows values under 2^-110 have products below fp32's normal numbers.
+// reference goes 2^16 beyond the maximum, as scores that rose once tend to rise again: 8 heads x
+// 8192 x 8192 with scores that rise by 25 nats over the keys take 280 us, 418 if it went to the
+// maximum (by 100 nats: 286 and 461; 264 and 277 with the limit of 2^24).  What that costs is the
+// lower end: in such rows values under 2^-110 have products below fp32's normal numbers.
 //
 // One CTA works on one head, one 128-row query tile and one slice of the key tiles.  12 warps:
 // 0-3 / 4-7 the softmax groups, which take the even and the odd key tiles (warp w owns TMEM lanes
@@ -35,23 +35,34 @@
 // product, as 0 * NaN would not be 0: those past the hull of the ranges, and, where the ranges of
 // neighbouring rows do not touch (padding between segments), those in the gaps.
 //
-// What bounds it.  Few rows: reading K and V once (24 heads x 60480 keys, one row: 109 us =
-// 6.8 TB/s, and 4 us for the join of the slices that the keys are split into).  Many rows: the
-// exponentials, with the tensor pipe at 63% of its cycles.  Two softmax warps share a scheduler
-// and take about 1700 cycles a tile each, of which 700 are the special-function unit's (88 of the
-// 128 exponentials of a row's tile; the others by polynomial) and the rest the latencies of some
-// 700 instructions in order; the MMAs of a tile take 1024 cycles, and reading Q, K, V and writing
-// K, V in shared memory 1280.  24 heads x 30240 x 30240 take 9.05 ms alone (1241 TFLOP/s) and
-// 9.7 to 10.0 ms in a loop at the 1000 W power cap (1126 to 1163 TFLOP/s, 1470 MHz).
+// p is rounded to bf16 because the tensor cores take P and V in one type and V is bf16; a P of two
+// bf16 parts would double the second product.  The sums l stay fp32 and take p unrounded.  Against
+// 64 bits the relative error of a bf16 output is 2.3e-3, where the rounding of the output alone
+// is 1.7e-3.
+//
+// What bounds it.  Few rows: reading K and V once (24 heads x 60480 keys, one row: 116 us =
+// 6.4 TB/s, and 5 us for the join of the slices that the keys are split into).  Many rows, d = 128:
+// no unit, but two chains of about the same length.  A key tile takes 1514 cycles (the slope of a
+// CTA's cycles over the keys; 1606 with its start and end).  The MMA warp needs nearly all of them,
+// 1480 by clock stamps: 1150 to issue the tile's 16 MMAs (which execute in 1024; their operands and
+// the loads of K, V take 1280 of shared memory's cycles), 150 for a barrier test that has long come
+// true and 180 around them.  A softmax warp has one tile in two such periods and is busy for 2670
+// of the 2960 cycles: 1800 to load the scores and exponentiate, 330 for its turn, 230 for the
+// reference, 140 to store P, 170 to see S.  The special-function unit works 700 of a period's
+// cycles (88 of the 128 exponentials of a row's tile; the others by polynomial), and a scheduler
+// issues in half of them (840 instructions a tile).  d = 64: the products halve, the softmax does
+// not, and a tile takes 1570 cycles by the stamps.
+// 24 heads x 30240 x 30240 take 8.6 to 9.05 ms alone (1305 to 1241 TFLOP/s) and 9.7 to 10.0 ms in
+// a loop at the 1000 W power cap (1126 to 1163 TFLOP/s, 1470 MHz); with d = 64 7.7 ms and 8.1 ms.
 //
 // The steps, on that case unless named: running maximum, pair of query tiles per CTA 10.9 ms;
 // no maximum per tile 10.3; registers moved to the softmax warps, polynomial 9.7; tile waits in a
 // warp of their own 9.3 (a barrier test takes a few hundred cycles while the MMAs read shared
 // memory); one query tile per CTA, three S buffers, common reference 9.5 against 10.6 on one box,
-// and packed prompts 58 -> 40 us; late query tiles first 285 -> 272 us (8191 causal rows); masks
-// over the scores instead of in the exponentials 10.0 -> 9.7.
+// and packed prompts 58 -> 40 us; late query tiles first 327 -> 310 us (8191 causal rows, in a
+// loop); masks over the scores instead of in the exponentials 10.0 -> 9.7.
 // Measured and not kept: S in 64-key units (an M = 128 MMA takes 64 cycles for N = 64 too), P
-// handed over in halves, CTA pairs with M = 256 (no faster: the exponentials bound both).
+// handed over in halves, CTA pairs with M = 256 (no faster, though they halve the reads of K, V).
 //
 // Every wait is bounded (see spark_ptx.cuh); on expiry the kernel flags kErrTimeout, drains its
 // copies and MMAs, frees TMEM and returns.
@@ -67,14 +78,15 @@ namespace {
 constexpr int kWarpLoad = 8, kWarpMma = 9, kWarpTiles = 10;
 constexpr int kThreads = 384;                // three warpgroups; warp 11 only gives registers
 // Registers a thread: 168 at launch (all the SM has for 384 threads), then moved from the third
-// warpgroup to the softmax ones; 2 * kRegsSoftmax + kRegsOther == 3 * kRegsLaunch.
+// warpgroup to the softmax ones; 2 * kRegsSoftmax + kRegsOther == 3 * kRegsLaunch.  The softmax is
+// a few short at its peak: 20 bytes are spilled (24 for d = 64).
 constexpr int kRegsLaunch = 168, kRegsSoftmax = 208, kRegsOther = 88;
 static_assert(2 * kRegsSoftmax + kRegsOther == 3 * kRegsLaunch, "register split");
 constexpr uint32_t kColO = 384;              // S/P buffers at TMEM columns 0, 128, 256
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kMaxSum = 0x1p8f;            // a tile's sum of p from which the reference is raised
-constexpr float kRoom = 16.f;                // powers of two a raised reference is put above the maximum
+constexpr float kRoom = 16.f;                // powers of two from the maximum to a raised reference
 constexpr int kMaxSplits = 64;
 constexpr int kPolyEvery = 3;                // every third pair of exponentials by polynomial
 
@@ -154,10 +166,10 @@ __device__ __forceinline__ float max3_nan(float a, float b, float c) {
 
 // 2^a of two values without the special-function unit: 2^a = 2^n 2^f, n the nearest integer
 // (taken by adding 1.5 * 2^23, which leaves n in the low bits), 2^f on [-1/2, 1/2] by a degree-4
-// polynomial that is 1 at 0, fitted for the least largest relative error (2.9e-6 in fp32; the result
-// is rounded to bf16, 2^-9).  Arguments from -127 down give 0 exactly (n = -127 takes the exponent of
-// 1.0 away), so that a masked key adds none of its value, however large.  Those from 128 on and NaN
-// give anything: `top`, the largest argument so far, tells the caller.
+// polynomial that is 1 at 0, fitted for the least largest relative error (2.9e-6 in fp32; the
+// result is rounded to bf16, 2^-8).  Arguments from -127 down give 0 exactly (n = -127 takes the
+// exponent of 1.0 away), so that a masked key adds none of its value, however large.  Those from 128
+// on and NaN give anything: `top`, the largest argument so far, tells the caller.
 __device__ __forceinline__ void ex2_poly2(uint64_t a2, float& top, float& p0, float& p1) {
   float a0, a1;
   f2_unpack(a2, a0, a1);
@@ -334,7 +346,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_dense_kernel(
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   const int h = blockIdx.z, split = blockIdx.y;
   // late query tiles first: under causal ranges they have the most keys, and a launch should not
-  // end with its longest CTAs (8191 causal rows, 16 heads: 285 -> 272 us)
+  // end with its longest CTAs (8191 causal rows, 16 heads, in a loop: 327 -> 310 us)
   const int q0 = static_cast<int>(gridDim.x - 1 - blockIdx.x) * 128;
 
   // This thread's row and its key ranges; rows past nq count as unmasked and are never stored.
@@ -833,7 +845,8 @@ static cudaError_t launch_dense_t(const DenseMaps& m, int H, int nq, int nk, int
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              static_cast<int>(smem));
     if (e != cudaSuccess) return e;
-    // the register split waits for registers that a launch with fewer would not have
+    // The register split would wait for ever for registers that a launch with fewer does not have:
+    // a compiler that gives the kernel fewer than it may use gets an error here.
     cudaFuncAttributes attr;
     e = cudaFuncGetAttributes(&attr, kern);
     if (e != cudaSuccess) return e;

@@ -16,8 +16,9 @@
 // asynchronous copies into shared memory: 4 under way per thread.  On 60480 tokens, 20 heads,
 // d = 128, bf16, Q, K and V from a fused projection, the steps to that measured 479 us (all
 // three tensors in a thread, loads into registers), 401 us (one tensor per CTA), 380 us
-// (accesses that cover whole sectors), 333 us (asynchronous copies) and 299 us = 6.2 TB/s
-// (streaming stores, 6 CTAs of 128 threads an SM), 95% of the measured copy bandwidth.
+// (accesses that cover whole sectors), 333 us (asynchronous copies) and 299 us (streaming stores,
+// 6 CTAs of 128 threads an SM).  It now takes 308 to 311 us in a loop = 6.0 TB/s, 91% of the
+// measured copy bandwidth.
 #include <type_traits>
 
 #include "spark_kernels.cuh"
@@ -70,8 +71,8 @@ __device__ __forceinline__ void cp_wait() {
 
 // V: values per access (the two halves of V pairs are V values each); C: such accesses per
 // thread and half; kPart: some vector of an interleaved row is rotated in part, which takes a test
-// per pair (with the test in every row 60480 tokens took 325 us in place of 306; without vectors
-// rotated in part, by narrower accesses, 16384 tokens with 33 pairs took 75 us in place of 40).
+// per pair (with the test in every row 60480 tokens took 6% longer; without vectors rotated in
+// part, by narrower accesses, 16384 tokens with 33 pairs took 75 us in place of 40).
 template <typename T, int D, int V, int C, bool kPart>
 __global__ void __launch_bounds__(kRopeThreads, kRopeCtas)
     qk_norm_rope_kernel(const RopeArgs a, int heads_per_cta) {

@@ -599,9 +599,9 @@ SPARK_API spark_status spark_rope_frequencies(const int32_t* axis_pairs, int nax
  *     the tile see and others mask adds nothing to the latter while it is finite; an infinity or
  *     NaN in it reaches them, as 0 * NaN.
  *   - bf16 tensor-core products with fp32 sums; probabilities are rounded to bf16.  The weighted
- *     values are summed in fp32 before they are divided by the sum of the weights: finite for values
- *     below 2^127 / (keys of the row, in whole tiles of 128); larger ones may overflow.  Those under
- *     2^-110 may count as 0. */
+ *     values are summed in fp32 before they are divided by the sum of the weights: finite for
+ *     values below 2^127 / (keys of the row, in whole tiles of 128); larger ones may overflow.
+ *     Values under 2^-110 may count as 0. */
 #define SPARK_MAX_DENSE (1 << 30)
 
 /* Workspace bytes of spark_attend_dense; 0 if the sizes are invalid. */
