@@ -206,11 +206,12 @@ def _empty(shape, dtype, device, stream):
     """torch.empty for a call on `stream`, from that stream's pool: memory of the current stream's
     could still be in use there, or be handed out again, while the call works on it.  The current
     stream is where the caller reads and drops it."""
-    if stream is None:
+    current = None if stream is None else torch.cuda.current_stream(device)
+    if stream == current:
         return torch.empty(shape, dtype=dtype, device=device)
     with torch.cuda.stream(stream):
         t = torch.empty(shape, dtype=dtype, device=device)
-    t.record_stream(torch.cuda.current_stream(device))
+    t.record_stream(current)
     return t
 
 
@@ -867,6 +868,7 @@ def spark_bsa_forward_host(Q, K, V, q_perm, k_perm, q_offsets, k_offsets, topk_r
     _need_host(out, "out", Q.dtype)
     if streams is None:
         streams = (torch.cuda.current_stream(dev), torch.cuda.Stream(dev), torch.cuda.Stream(dev))
+    streams = tuple(streams)
     if staging is None:                  # the copy streams start and end within the compute stream
         staging = _empty(spark_bsa_host_staging_size_ex(H, N, d, Q.dtype, nqb, nkb, hpc, nc),
                          torch.uint8, dev, streams[0])

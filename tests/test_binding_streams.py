@@ -106,6 +106,21 @@ CALLS = {
 }
 
 
+def test_streams_of_the_host_pipeline_may_be_any_iterable(made):
+    bsa.spark_bsa_forward_host(*host(9), 0.5, out=host(9)[0], streams=iter([SIDE, MAIN, MAIN]))
+    assert [t.made_on for t in made] == [SIDE] * 2
+
+
+@pytest.mark.parametrize("name", CALLS)
+def test_the_current_stream_given_is_no_other_stream(made, name, monkeypatch):
+    def switched(stream):
+        raise AssertionError("switched streams")
+
+    monkeypatch.setattr(torch.cuda, "stream", switched)
+    CALLS[name][1](MAIN)
+    assert all(t.used_on is None for t in made) and len(made) == CALLS[name][0]
+
+
 @pytest.mark.parametrize("name", CALLS)
 def test_allocations_come_from_the_stream_of_the_call(made, name):
     count, call = CALLS[name]
