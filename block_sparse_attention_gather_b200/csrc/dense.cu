@@ -168,8 +168,8 @@ __device__ __forceinline__ float max3_nan(float a, float b, float c) {
 // (taken by adding 1.5 * 2^23, which leaves n in the low bits), 2^f on [-1/2, 1/2] by a degree-4
 // polynomial that is 1 at 0, fitted for the least largest relative error (2.9e-6 in fp32; the
 // result is rounded to bf16, 2^-8).  Arguments from -127 down give 0 exactly (n = -127 takes the
-// exponent of 1.0 away), so that a masked key adds none of its value, however large.  Those from 128
-// on and NaN give anything: `top`, the largest argument so far, tells the caller.
+// exponent of 1.0 away), so that a masked key adds none of its value, however large.  Those from
+// 128 on and NaN give anything: `top`, the largest argument so far, tells the caller.
 __device__ __forceinline__ void ex2_poly2(uint64_t a2, float& top, float& p0, float& p1) {
   float a0, a1;
   f2_unpack(a2, a0, a1);
